@@ -71,8 +71,9 @@ typedef enum {
   VATTN_ERR_CUDA = -5,
   VATTN_ERR_DEVICE_TIMEOUT = -6,
   VATTN_ERR_WORKSPACE = -7,
-  VATTN_ERR_DEVICE_BOUNDS = -8   /* debug build only: a kernel computed an out-of-range row, tile or
-                                    coordinate, skipped the access and stopped (vattn_get_status) */
+  VATTN_ERR_DEVICE_BOUNDS = -8   /* a cache kernel read an index out of range, or (debug build only) a
+                                    kernel computed an out-of-range row, tile or coordinate; it skipped
+                                    the access (vattn_get_status) */
 } vattn_status;
 
 /* Operation ids for vattn_workspace_size. */
@@ -351,12 +352,125 @@ int vattn_dual_bwd(const vattn_geom* geom, const void* q, const void* k, const v
                    float scale, void* dq, void* dk, void* dv, float* dg, void* workspace,
                    size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit key/value cache: attention for generation that runs chunk by chunk (a
+ * latent frame, or a token, at a time), where new queries attend to the keys
+ * and values of everything generated before.
+ *
+ * The cache is a pool of pages shared by any number of streams.  A page holds
+ * page_tokens tokens of every kv head:
+ *   kcache, vcache  e4m3 bytes [pages][kv_heads][page_tokens][d]
+ *   kscale, vscale  float32    [pages][kv_heads][page_tokens / 16]
+ * with one scale, a power of two, for each block of 16 tokens and kv head:
+ * value = byte * scale.  A token's slot is page * page_tokens + its row in the
+ * page.  block_table (int32 [streams][table_width]) lists each stream's pages
+ * in token order: token p of stream s is row p % page_tokens of page
+ * block_table[s][p / page_tokens].
+ *
+ * Token tensors (q, k, v, o) are bf16 [n_tokens][heads][d], the streams' new
+ * tokens one after the other: stream s owns tokens q_starts[s] ..
+ * q_starts[s + 1] - 1.  q, k and v may be slices of a fused projection: their
+ * token stride (in elements, a multiple of 8, at least heads * d) is an
+ * argument.  q_heads is a multiple of kv_heads; query head h reads kv head
+ * h / (q_heads / kv_heads).
+ *
+ * Frame-causal mask: token i of a stream's n new tokens has position
+ * p = kv_len - n + i.  frame_tokens = 0: it sees every cached token of its
+ * stream.  frame_tokens = F > 0: with f = floor(p / F) it sees the tokens of
+ * frames up to its own, positions below min(kv_len, (f + 1) F) (F = 1 is the
+ * token-causal mask); window_frames = W > 0 keeps the last W frames only,
+ * positions from max(0, (f - W + 1) F).  A token that sees nothing gets O = 0
+ * and LSE = -inf.
+ *
+ * Limits (VATTN_ERR_UNSUPPORTED otherwise): head_dim 64 or 128, page_tokens 16,
+ * 32, 64 or 128, q_heads <= 65535, pages * page_tokens < 2^31, streams <=
+ * 65535.  Indices that the kernels read from device memory (q_starts, kv_lens,
+ * block_table, slots) are checked there: one out of range is never
+ * dereferenced, VATTN_ERR_DEVICE_BOUNDS is recorded (vattn_get_status) and the
+ * outputs of the stream concerned are unspecified.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int64_t streams, q_heads, kv_heads, head_dim;
+  int64_t pages;          /* pages in the pool */
+  int32_t page_tokens;    /* tokens in a page */
+  int32_t table_width;    /* block_table entries per stream */
+  int32_t frame_tokens;   /* F of the mask; 0 = no mask */
+  int32_t window_frames;  /* W of the mask; 0 = no window */
+} vattn_cache_geom;
+
+/* result[0] of vattn_cache_plan. */
+enum {
+  VATTN_PLAN_OK = 0,
+  VATTN_PLAN_NO_PAGES = 1,    /* the pool has too few free pages */
+  VATTN_PLAN_TABLE_FULL = 2,  /* a stream outgrows its block_table row */
+  VATTN_PLAN_NO_SLOTS = 3,    /* more new tokens than max_tokens */
+  VATTN_PLAN_BAD_STATE = 4    /* a length, count or page id that cannot be */
+};
+
+/* Plans one step of every stream on the device: gives each stream the pages
+ * its new tokens need and lists every new token's slot.
+ *   new_tokens int32 [streams]: tokens added to the stream (0: none; negative:
+ *     the stream ends, its pages return to the pool and its length becomes 0);
+ *   kv_lens int32 [streams]: tokens held before; block_table: extended in place;
+ *   free_pages int32 [pages], n_free int32 [1]: stack of free pages, top at
+ *     n_free - 1.  Pages of ending streams are pushed first, in stream order,
+ *     then pages are popped in stream order, so the result is deterministic.
+ * Outputs: kv_lens_out [streams] (may be kv_lens) and n_free_out [1] (may be
+ * n_free); q_starts int32 [streams + 1], the running sum of the new tokens;
+ * slots int32 [max_tokens], -1 past the last new token; result int32 [4] =
+ * {VATTN_PLAN_*, new tokens, free pages left, longest stream}.
+ * All or nothing: unless result[0] is VATTN_PLAN_OK the state is unchanged,
+ * q_starts is all 0 and slots all -1, so that vattn_cache_append and
+ * vattn_cache_fwd on them do nothing.  Apart from the two pairs named, the
+ * arrays must not overlap. */
+int vattn_cache_plan(const vattn_cache_geom* geom, const int32_t* new_tokens, const int32_t* kv_lens,
+                     int32_t* block_table, int32_t* free_pages, const int32_t* n_free, int32_t* kv_lens_out,
+                     int32_t* n_free_out, int32_t* q_starts, int32_t* slots, int64_t max_tokens, int32_t* result,
+                     void* stream);
+
+/* Quantises new keys and values into their slots.  For each 16-token block and
+ * kv head that gets tokens: with e(t) the smallest e >= -40 such that every
+ * element of token t's row is at most 448 * 2^e (448: the largest e4m3), the
+ * block's scale becomes 2^E, E = max over its new tokens' e(t) and, when it
+ * held tokens before, its old exponent; new bytes are rne_e4m3(x * 2^-E); the
+ * bytes held before are rescaled to the new scale; the rows behind the last
+ * token become 0.  A scale that is a power of two costs an e4m3 value no
+ * precision (it is a floating format), and rescaling is exact down to the
+ * subnormals.  A token whose k or v row of a kv head holds a NaN or an infinity
+ * is stored as NaN keys and zero values for that head: outputs that see it are
+ * NaN, all others are untouched.
+ * slots: as vattn_cache_plan lists them: ascending within a 16-token block,
+ * and a block's new tokens directly follow those that it holds; negative
+ * entries are skipped.  A slot must not be listed twice. */
+int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, const int32_t* slots, int64_t n_tokens, void* kcache, void* vcache,
+                       float* kscale, float* vscale, void* stream);
+
+/* Attention of the streams' new tokens over the cache (append them first):
+ * S = scale * q.k over the tokens that the mask leaves, LSE = ln sum exp(S),
+ * O = sum exp(S - LSE) v.  scale must be positive and finite.
+ *   max_new: no stream has more new tokens than this (the caller knows it
+ *     without reading device memory); it selects the kernel and sizes the grid;
+ *   o bf16 [n_tokens][q_heads][d], lse float32 [n_tokens][q_heads] or NULL.
+ *     Rows behind the last stream's tokens are not written.
+ *   workspace >= vattn_cache_workspace_size(geom, n_tokens, max_new): partial
+ *     results of keys that are split over several thread blocks.  Two calls
+ *     that may overlap on the GPU need a workspace each.
+ * A query row with a NaN or an infinity gives a NaN row.  Deterministic. */
+int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_stride, const int32_t* q_starts,
+                    const int32_t* kv_lens, const int32_t* block_table, const void* kcache, const void* vcache,
+                    const float* kscale, const float* vscale, float scale, int64_t n_tokens, int64_t max_new,
+                    void* o, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Scratch bytes that vattn_cache_fwd needs. */
+int vattn_cache_workspace_size(const vattn_cache_geom* geom, int64_t n_tokens, int64_t max_new, size_t* bytes);
+
 /* Scratch bytes that `op` needs for `geom` (0 if none). */
 int vattn_workspace_size(int op, const vattn_geom* geom, size_t* bytes);
 
 /* Synchronises `stream`, reads and clears the library's device error word and
- * the CUDA error state.  Returns VATTN_OK, VATTN_ERR_DEVICE_TIMEOUT or
- * VATTN_ERR_CUDA. */
+ * the CUDA error state.  Returns VATTN_OK, VATTN_ERR_DEVICE_TIMEOUT,
+ * VATTN_ERR_DEVICE_BOUNDS or VATTN_ERR_CUDA. */
 int vattn_get_status(void* stream);
 
 /* Message for the last non-OK return on this thread ("" if none). */

@@ -40,6 +40,11 @@ VATTN_OP_HIER_BWD = 8
 VATTN_OP_STA_FWD_FP8 = 9
 VATTN_OP_DUAL_FWD_FP8 = 10
 VATTN_OP_DUAL_SYM_LEARNED_FWD = 11
+VATTN_PLAN_OK = 0
+VATTN_PLAN_NO_PAGES = 1
+VATTN_PLAN_TABLE_FULL = 2
+VATTN_PLAN_NO_SLOTS = 3
+VATTN_PLAN_BAD_STATE = 4
 VATTN_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 VATTN_DEBUG_SKIP_ARRIVAL = 1
@@ -76,12 +81,33 @@ def make_geom(batch: int, heads: int, head_dim: int, grid: Sequence[int], tile: 
     return g
 
 
+class CacheGeom(ctypes.Structure):
+    _fields_ = [
+        ("streams", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("pages", ctypes.c_int64),
+        ("page_tokens", ctypes.c_int32),
+        ("table_width", ctypes.c_int32),
+        ("frame_tokens", ctypes.c_int32),
+        ("window_frames", ctypes.c_int32),
+    ]
+
+
+def make_cache_geom(streams: int, q_heads: int, kv_heads: int, head_dim: int, pages: int, page_tokens: int,
+                    table_width: int, frame_tokens: int = 0, window_frames: int = 0) -> CacheGeom:
+    return CacheGeom(streams, q_heads, kv_heads, head_dim, pages, page_tokens, table_width, frame_tokens,
+                     window_frames)
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _INT = ctypes.c_int
 _GP = ctypes.POINTER(Geom)
+_CP = ctypes.POINTER(CacheGeom)
 
 _SIGS = {
     "vattn_tile_permute": [_GP, _P, _P, _I64, _P],
@@ -115,12 +141,20 @@ _SIGS = {
     "vattn_version": [],
 }
 
+# The 8-bit key/value cache (its geometry is a vattn_cache_geom).
+_CACHE_SIGS = {
+    "vattn_cache_plan": [_CP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P],
+    "vattn_cache_append": [_CP, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P],
+    "vattn_cache_fwd": [_CP, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _F, _I64, _I64, _P, _P, _P, _SZ, _P],
+    "vattn_cache_workspace_size": [_CP, _I64, _I64, ctypes.POINTER(_SZ)],
+}
+
 
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python video_dit_local_b200/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, args in _SIGS.items():
+    for name, args in (*_SIGS.items(), *_CACHE_SIGS.items()):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_char_p if name in ("vattn_last_error", "vattn_version") else ctypes.c_int
@@ -330,6 +364,67 @@ def vattn_workspace_size(op: int, geom: Geom) -> int:
     n = _SZ(0)
     _check(lib.vattn_workspace_size(op, ctypes.byref(geom), ctypes.byref(n)))
     return n.value
+
+
+def _tokens(x, what: str):
+    """(address, token stride, tokens) of a [tokens, heads, d] CUDA tensor whose
+    tokens' rows are dense (a slice of a fused projection along dim 1 is)."""
+    if not x.is_cuda:
+        raise ValueError(f"{what} got a host tensor: pass a CUDA tensor")
+    n, heads, d = x.shape
+    if x.stride(2) != 1 or x.stride(1) != d:
+        raise ValueError(f"{what}: heads and channels of a token must be contiguous")
+    return x.data_ptr(), x.stride(0) if n > 1 else heads * d, n
+
+
+def _same_device(*tensors) -> None:
+    """The kernels run on the current device's stream: every tensor must live there."""
+    devices = {x.get_device() for x in tensors if x is not None and not isinstance(x, int)}
+    if not devices:
+        return
+    import torch
+    if len(devices) > 1 or (torch.cuda.is_available() and devices != {torch.cuda.current_device()}):
+        raise ValueError(f"tensors on devices {sorted(devices)}: all must be on the current device")
+
+
+def vattn_cache_plan(geom: CacheGeom, new_tokens, kv_lens, block_table, free_pages, n_free, kv_lens_out, n_free_out,
+                     q_starts, slots, result, max_tokens: Optional[int] = None, stream=None) -> None:
+    """Pages and slots of one step's new tokens (int32 tensors; max_tokens defaults to the length of slots)."""
+    _same_device(new_tokens, kv_lens, block_table, free_pages, n_free, kv_lens_out, n_free_out, q_starts, slots,
+                 result)
+    _check(lib.vattn_cache_plan(ctypes.byref(geom), _ptr(new_tokens), _ptr(kv_lens), _ptr(block_table),
+                                _ptr(free_pages), _ptr(n_free), _ptr(kv_lens_out), _ptr(n_free_out), _ptr(q_starts),
+                                _ptr(slots), slots.numel() if max_tokens is None else max_tokens, _ptr(result),
+                                _stream(stream)))
+
+
+def vattn_cache_append(geom: CacheGeom, k, v, slots, kcache, vcache, kscale, vscale, stream=None) -> None:
+    """Quantise k, v [tokens, kv_heads, d] (bf16, may be slices of a fused projection) into their slots."""
+    _same_device(k, v, slots, kcache, vcache, kscale, vscale)
+    kp, ks, n = _tokens(k, "k")
+    vp, vs, nv = _tokens(v, "v")
+    if nv != n or slots.numel() < n:
+        raise ValueError(f"{n} keys, {nv} values and {slots.numel()} slots")
+    _check(lib.vattn_cache_append(ctypes.byref(geom), kp, ks, vp, vs, _ptr(slots), n, _ptr(kcache), _ptr(vcache),
+                                  _ptr(kscale), _ptr(vscale), _stream(stream)))
+
+
+def vattn_cache_workspace_size(geom: CacheGeom, n_tokens: int, max_new: int) -> int:
+    n = _SZ(0)
+    _check(lib.vattn_cache_workspace_size(ctypes.byref(geom), n_tokens, max_new, ctypes.byref(n)))
+    return n.value
+
+
+def vattn_cache_fwd(geom: CacheGeom, q, q_starts, kv_lens, block_table, kcache, vcache, kscale, vscale, scale: float,
+                    max_new: int, o, lse=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    """Attention of q [tokens, q_heads, d] (bf16, may be a slice of a fused projection) over the cache."""
+    _same_device(q, q_starts, kv_lens, block_table, kcache, vcache, kscale, vscale, o, lse, workspace)
+    if workspace is not None and not ws_bytes:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    qp, stride, n = _tokens(q, "q")
+    _check(lib.vattn_cache_fwd(ctypes.byref(geom), qp, stride, _ptr(q_starts), _ptr(kv_lens), _ptr(block_table),
+                               _ptr(kcache), _ptr(vcache), _ptr(kscale), _ptr(vscale), scale, n, max_new, _ptr(o),
+                               _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def vattn_get_status(stream=None) -> int:

@@ -637,7 +637,8 @@ int vattn_get_status(void* stream) {
     const int zero = 0;
     e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e, "clear device error word");
-    return fail(word, "device reported status %d (a bounded wait ran out)", word);
+    return fail(word, "device reported status %d (%s)", word,
+                word == VATTN_ERR_DEVICE_BOUNDS ? "an index out of range" : "a bounded wait ran out");
   }
   return ok();
 }
