@@ -123,6 +123,11 @@ struct CacheAppendArgs {
 };
 cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, cudaStream_t st);
 
+// -- cache_attn_few.cu: max_new * group <= 16 query rows per stream and kv head --
+bool cache_few_fits(const cache::Geom& g, long long max_new);
+size_t cache_few_workspace(const cache::Geom& g);
+cudaError_t launch_cache_few(const cache::FwdParams& p, void* workspace, cudaStream_t st);
+
 // -- cache_attn.cu --
 size_t cache_fwd_workspace(const cache::Geom& g, long long n_tokens, long long max_new);
 cudaError_t launch_cache_fwd(const cache::FwdParams& p, void* workspace, cudaStream_t st);

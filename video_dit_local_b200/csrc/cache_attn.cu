@@ -90,10 +90,13 @@ __global__ void __launch_bounds__(128) rows_kernel(const FwdParams p) {
 
 }  // namespace cache
 
-size_t cache_fwd_workspace(const cache::Geom&, long long, long long) { return 0; }
+size_t cache_fwd_workspace(const cache::Geom& g, long long, long long max_new) {
+  return cache_few_fits(g, max_new) ? cache_few_workspace(g) : 0;
+}
 
-cudaError_t launch_cache_fwd(const cache::FwdParams& p, void*, cudaStream_t st) {
+cudaError_t launch_cache_fwd(const cache::FwdParams& p, void* ws, cudaStream_t st) {
   using namespace cache;
+  if (cache_few_fits(p.g, p.max_new)) return launch_cache_few(p, ws, st);
   const dim3 grid(p.n_tokens, p.g.q_heads);
   if (p.g.d == 128)
     rows_kernel<128><<<grid, 128, 0, st>>>(p);

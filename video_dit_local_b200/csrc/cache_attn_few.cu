@@ -1,0 +1,596 @@
+// Attention over the 8-bit key/value cache for few query rows: the new tokens
+// of a stream times the query heads of a kv head make at most 16 rows.
+//
+// Bound by HBM: 2 d bytes for every key and kv head, read once, against 4 d
+// flop for each row.  So the design serves the loads:
+//  - every warp streams its own 32-key steps through a private ring in shared
+//    memory with 16-byte asynchronous copies: no barrier between warps, and
+//    three thread blocks of four warps keep about 100 KB in flight on an SM,
+//    twice what the memory latency needs at full rate;
+//  - a fixed grid shares all streams' 128-key tiles evenly, whatever their
+//    lengths: thread block c of C takes tiles [c T / C, (c + 1) T / C) of the T
+//    tiles laid out stream by stream and head by head.  A (stream, head) that
+//    spans several thread blocks leaves partial results that a second kernel
+//    joins in a fixed order; it is launched early (programmatic dependent
+//    launch) so that only its joins are exposed.
+//  - the products run on mma.sync m16n8k16: 16 rows are far too few for a
+//    tcgen05 tile, the operands come from registers as they are converted, and
+//    the tensor pipe idles most of the time anyway.
+//
+// Numbers: e4m3 bytes become f16 exactly.  A query row is scaled by a power of
+// two into f16's upper range, so its 8 significant bits are exact down to
+// 2^-29 of the row's largest element.  P is kept in (0, 2^14] as f16, 11
+// significant bits down to 2^-28 of the row's largest weight.  A V scale is a
+// power of two: it enters the exponent of P, x_j = s_j + log2(vs), and the row
+// sum takes P 2^-log2(vs), so that O needs no scale and no weight overflows.
+#include "cache.cuh"
+
+namespace vattn {
+namespace cache {
+namespace few {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int STEP = 32;             // keys of a warp's step
+constexpr int TILE = WARPS * STEP;   // keys of a thread block's step
+constexpr int ROWS = 16;
+constexpr int CTAS_PER_SM = 3;
+constexpr int GRID = 148 * CTAS_PER_SM;
+constexpr float P_SHIFT = 14.0f;     // P = 2^(x - m + 14)
+
+// Two partial results a thread block: of the (stream, head) that began before
+// its tiles (slot 0) and of the one that goes on after them (slot 1).
+constexpr int SLOTS = GRID * 2;
+inline size_t workspace_bytes(int d) { return (size_t)SLOTS * ROWS * (d + 2) * sizeof(float); }
+__device__ __forceinline__ float* slot_o(void* ws, int d, int slot) { return (float*)ws + (size_t)slot * ROWS * d; }
+__device__ __forceinline__ float2* slot_ml(void* ws, int d, int slot) {
+  return (float2*)((float*)ws + (size_t)SLOTS * ROWS * d) + (size_t)slot * ROWS;
+}
+
+template <int D>
+struct Ring {
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int HALF = STEP * D;                     // K or V bytes of a step
+  static constexpr int SCALES = 16;                         // 2 K and 2 V scales
+  static constexpr int STAGE = 2 * HALF + SCALES;
+  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int MERGE = ROWS * D * 4 + ROWS * 8;     // a warp's partial result, over its own ring
+  static constexpr int PER_WARP = WARP > MERGE ? WARP : MERGE;
+  static constexpr int TOTAL = WARPS * PER_WARP;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;  // 0: the 16 bytes become zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Shared-memory layouts of a step.  Lane (g, t) = (lane / 4, lane % 4) of the
+// MMA fragments reads, eight lanes (two g, four t) at a time:
+//  K: 16 bytes at chunk t (+ 4) of row ... + (g & 1): at d = 128 odd rows keep
+//     their chunks 4 further on, so that the eight lanes meet all 32 banks
+//     (at d = 64 two rows fill them anyway);
+//  V: chunk g of rows 4 t + r: chunks are turned by 2 (row / 4).  d = 64: 8-byte
+//     reads by 16 lanes; rows 4..7 and 12..15 swap with their neighbours and
+//     rows 8..15 turn by two chunks.
+template <int D>
+__device__ __forceinline__ uint32_t k_at(int row, int chunk) {
+  return D == 128 ? row * 128 + ((chunk ^ ((row & 1) << 2)) << 4) : row * 64 + (chunk << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_at(int row, int chunk) {
+  return D == 128 ? row * 128 + ((chunk ^ (((row >> 2) & 3) << 1)) << 4)
+                  : (row ^ ((row >> 2) & 1)) * 64 + ((chunk ^ (((row >> 3) & 1) << 1)) << 4);
+}
+
+// Thread blocks that share `total` tiles, each with one at least: block c
+// takes tiles [c total / sharers, (c + 1) total / sharers).
+__device__ __forceinline__ int sharers(long long total) { return (int)min((long long)GRID, total); }
+
+// The tiles of one stream, for each kv head: keys [base, end), `tiles` of TILE.
+struct StreamTiles {
+  StreamStep st;
+  int base, end, tiles;
+};
+__device__ __forceinline__ StreamTiles stream_tiles(const FwdParams& p, int s) {
+  StreamTiles r;
+  r.st = stream_step(p, s);
+  r.base = r.end = r.tiles = 0;
+  if (r.st.n > 0) {
+    int lo, hi, x;
+    key_range(p.g, r.st, 0, &lo, &x);
+    key_range(p.g, r.st, r.st.n - 1, &x, &hi);
+    r.base = lo & ~(STEP - 1);
+    r.end = max(hi, r.base);
+    r.tiles = max(1, (r.end - r.base + TILE - 1) / TILE);  // one that is empty still writes its rows
+  }
+  return r;
+}
+
+// Finds the stream of tile `want` (of all heads' tiles, stream by stream): its
+// index, its first tile, and the total.  All threads of the block take part.
+struct Place {
+  int stream;
+  long long first, total;
+};
+template <int NT, class Wanted>
+__device__ __forceinline__ Place find_stream(const FwdParams& p, Wanted wanted, long long* sums, Place* out) {
+  const int t = threadIdx.x;
+  const int per = (p.g.streams + NT - 1) / NT;
+  const int s0 = min(t * per, p.g.streams), s1 = min(s0 + per, p.g.streams);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) mine += stream_tiles(p, s).tiles;
+  mine *= p.g.kv_heads;
+  long long x = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, x, o);
+    if ((t & 31) >= o) x += y;
+  }
+  if ((t & 31) == 31) sums[t >> 5] = x;
+  __syncthreads();
+  long long before = x - mine, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < (t >> 5)) before += sums[w];
+    total += sums[w];
+  }
+  const long long want = wanted(total);
+  if (want >= before && want < before + mine) {
+    int s = s0;
+    for (;; ++s) {
+      const long long n = (long long)stream_tiles(p, s).tiles * p.g.kv_heads;
+      if (want < before + n) break;
+      before += n;
+    }
+    out->stream = s;
+    out->first = before;
+  }
+  __syncthreads();
+  Place r = *out;
+  r.total = total;
+  return r;
+}
+
+// UP: rows 8..15 exist.
+template <int D, bool UP>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdParams p, void* ws) {
+  using R = Ring<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long sums[WARPS];
+  __shared__ Place place;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Geom& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int fg = lane >> 2, ft = lane & 3;
+  uint8_t* mine = smem + warp * R::PER_WARP;
+  const uint32_t ring = smem_u32(mine);
+
+  const Place pl = find_stream<THREADS>(
+      p, [](long long total) { return blockIdx.x < sharers(total) ? blockIdx.x * total / sharers(total) : -1; }, sums,
+      &place);
+  const int share = sharers(pl.total);
+  if ((int)blockIdx.x >= share) return;
+  long long at = blockIdx.x * pl.total / share;
+  const long long stop = (blockIdx.x + 1) * pl.total / share;
+  int s = pl.stream;
+  long long first = pl.first;  // first tile of stream s
+  StreamTiles sp = stream_tiles(p, s);
+
+  while (at < stop) {
+    while (at >= first + (long long)sp.tiles * g.kv_heads) {
+      first += (long long)sp.tiles * g.kv_heads;
+      sp = stream_tiles(p, ++s);
+    }
+    const int h = (int)((at - first) / sp.tiles);
+    const int k0 = (int)((at - first) % sp.tiles);
+    const int k1 = (int)min((long long)sp.tiles, k0 + (stop - at));
+    at += k1 - k0;
+    const int rows = sp.st.n * g.group;
+
+    // query rows fg and fg + 8 as f16 MMA fragments, each row scaled by a power of two
+    uint32_t qf[D / 16][4];
+    float c_row[2], poison[2];
+    int lo[2], hi[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = fg + 8 * u;
+      const bool in = r < rows && (u == 0 || UP);
+      const int tok = in ? r / g.group : 0;
+      const __nv_bfloat16* src = p.q + (long long)(sp.st.row0 + tok) * p.q_stride +
+                                 (long long)(h * g.group + (in ? r - tok * g.group : 0)) * D;
+      uint2 w[D / 16];
+      uint32_t m = 0;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        w[kk] = in ? __ldg((const uint2*)(src + (kk >> 2) * 64 + 16 * ft + 4 * (kk & 3))) : make_uint2(0, 0);
+        m = __vmaxu2(m, __vmaxu2(w[kk].x & 0x7fff7fffu, w[kk].y & 0x7fff7fffu));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, __shfl_xor_sync(~0u, m, 1));
+      m = max(m, __shfl_xor_sync(~0u, m, 2));
+      poison[u] = m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
+      const int sh = m == 0 ? 0 : min(14 - ((int)(m >> 7) - 127), 126);
+      const float up = __int_as_float((sh + 127) << 23);
+      c_row[u] = p.scale_log2 * __int_as_float((127 - sh) << 23);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][u] = pack_f16(bf16lo(w[kk].x) * up, bf16hi(w[kk].x) * up);
+        qf[kk][u + 2] = pack_f16(bf16lo(w[kk].y) * up, bf16hi(w[kk].y) * up);
+      }
+      key_range(g, sp.st, tok, &lo[u], &hi[u]);
+    }
+    int all_lo, all_hi, x;  // keys that every row sees
+    key_range(g, sp.st, 0, &x, &all_hi);
+    key_range(g, sp.st, sp.st.n - 1, &all_lo, &x);
+    int min_lo, max_hi;
+    key_range(g, sp.st, 0, &min_lo, &x);
+    key_range(g, sp.st, sp.st.n - 1, &x, &max_hi);
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+
+    // steps of this warp: keys sp.base + (k * WARPS + warp) * STEP, k in [k0, k1)
+    const int* table = p.table + (long long)s * g.width;
+    auto step_key = [&](int k) { return sp.base + (k * WARPS + warp) * STEP; };
+    // page of the 16 keys from `key` on; -1: none of them is to be read
+    auto page_at = [&](int key) {
+      if (key >= max_hi || key + SCALE_TOKENS <= min_lo) return -1;
+      const int pg = __ldg(table + (key >> g.page_shift));
+      if ((unsigned)pg >= (unsigned)g.pages) {
+        report_error(p.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
+        return -1;
+      }
+      return pg;
+    };
+    int pg0 = -1, pg1 = -1;  // pages of the next step to be loaded
+    auto fetch_pages = [&](int k) {
+      if (k < k1) {
+        pg0 = page_at(step_key(k));
+        pg1 = page_at(step_key(k) + SCALE_TOKENS);
+      }
+    };
+    auto load = [&](int k) {
+      if (k < k1) {
+        const int key0 = step_key(k);
+        const uint32_t dst = ring + ((k - k0) % R::STAGES) * R::STAGE;
+        const int in_page = key0 & (g.page_tokens - 1);
+        const long long row0 = cache_row(g, max(pg0, 0), h, in_page);
+        // the second half lies in the same page unless pages hold 16 tokens
+        const long long row1 = cache_row(g, max(pg1, 0), h, (key0 + SCALE_TOKENS) & (g.page_tokens - 1));
+        constexpr int CH = D / 16, RP = 32 / CH;
+        const int c = lane % CH;
+#pragma unroll
+        for (int i = 0; i < STEP / RP; ++i) {
+          const int r = i * RP + lane / CH;
+          const bool second = i * RP >= SCALE_TOKENS;
+          const int key = key0 + r;
+          const bool in = (second ? pg1 : pg0) >= 0 && key < max_hi && key >= min_lo;
+          const long long off = ((second ? row1 - SCALE_TOKENS : row0) + r) * D + c * 16;
+          cp16(dst + k_at<D>(r, c), p.kc + (in ? off : 0), in);
+          cp16(dst + R::HALF + v_at<D>(r, c), p.vc + (in ? off : 0), in);
+        }
+        if (lane < 4) {
+          const bool in = (lane & 1 ? pg1 : pg0) >= 0;
+          const long long idx = in ? (lane & 1 ? row1 : row0) >> 4 : 0;
+          cp4(dst + 2 * R::HALF + lane * 4, (lane & 2 ? p.vs : p.ks) + idx, in);
+        }
+      }
+      cp_commit();
+    };
+    __syncwarp();
+    fetch_pages(k0);
+#pragma unroll
+    for (int i = 0; i < R::STAGES - 1; ++i) {
+      load(k0 + i);
+      fetch_pages(k0 + i + 1);
+    }
+    for (int k = k0; k < k1; ++k) {
+      load(k + R::STAGES - 1);
+      fetch_pages(k + R::STAGES);
+      cp_wait<R::STAGES - 1>();
+      __syncwarp();
+      const uint32_t st = ring + ((k - k0) % R::STAGES) * R::STAGE;
+      const int key0 = step_key(k);
+      if (key0 < max_hi) {
+        // S = Q K^T, 16 rows x 32 keys: column n of tile j is key
+        // 16 (j / 2) + 4 (n / 2) + 2 (j % 2) + n % 2, so that a thread's columns are the four keys
+        // whose V rows it reads
+        float sc[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+          const int r = 16 * (j >> 1) + 4 * (fg >> 1) + 2 * (j & 1) + (fg & 1);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 w = lds128(st + k_at<D>(r, ft + 4 * c));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma16816(sc[j], qf[c * 4 + e], e4m3x2_to_f16x2((uint16_t)(ww[e] & 0xffffu)),
+                       e4m3x2_to_f16x2((uint16_t)(ww[e] >> 16)));
+          }
+        }
+        float kf[2], ev[2], inv[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          kf[b] = lds32(st + 2 * R::HALF + b * 4);
+          const int e = (__float_as_int(lds32(st + 2 * R::HALF + 8 + b * 4)) >> 23) - 127;
+          ev[b] = (float)e;
+          inv[b] = __int_as_float((127 - max(e, -126)) << 23);
+        }
+        const bool whole = key0 >= all_lo && key0 + STEP <= all_hi;
+        uint32_t pf[2][4];  // P as MMA fragments, 16 keys each
+        bool moved = false;
+        float alpha[2] = {1.f, 1.f};
+#pragma unroll
+        for (int u = 0; u < (UP ? 2 : 1); ++u) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = fmaxf(c_row[u] * kf[j >> 1], 1.17549435e-38f), e = ev[j >> 1] + poison[u];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float v = fmaf(sc[j][2 * u + i], f, e);
+              if (!whole) {
+                const int key = key0 + 16 * (j >> 1) + 4 * ft + 2 * (j & 1) + i;
+                if (key < lo[u] || key >= hi[u]) v = -INFINITY;
+              }
+              sc[j][2 * u + i] = v;
+              mx = fmaxf(mx, v);
+            }
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+          if (mx > m_run[u]) {
+            alpha[u] = ex2(m_run[u] - mx);
+            m_run[u] = mx;
+            moved = true;
+          }
+          const float ref = (m_run[u] == -INFINITY ? 0.f : m_run[u]) - P_SHIFT;
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float a = ex2(sc[j][2 * u] - ref), b = ex2(sc[j][2 * u + 1] - ref);
+            sum[j >> 1] += a + b;
+            pf[j >> 1][(j & 1) * 2 + u] = pack_f16(a, b);
+          }
+          l_run[u] = l_run[u] * alpha[u] + (sum[0] * inv[0] + sum[1] * inv[1]);
+        }
+        if (!UP) {
+          pf[0][1] = pf[0][3] = pf[1][1] = pf[1][3] = 0;
+        }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][0] *= alpha[0];
+            o[j][1] *= alpha[0];
+            if (UP) {
+              o[j][2] *= alpha[1];
+              o[j][3] *= alpha[1];
+            }
+          }
+        }
+        // O += P V: column n = fg of channel tile j is channel (D / 8) fg + j
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t w[4][D / 32];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * ks + 4 * ft + r;
+            if constexpr (D == 128) {
+              const uint4 v = lds128(st + R::HALF + v_at<D>(row, fg));
+              w[r][0] = v.x;
+              w[r][1] = v.y;
+              w[r][2] = v.z;
+              w[r][3] = v.w;
+            } else {
+              const uint2 v = lds64(st + R::HALF + v_at<D>(row, fg >> 1) + (fg & 1) * 8);
+              w[r][0] = v.x;
+              w[r][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int q4 = 0; q4 < D / 32; ++q4) {
+            // four keys' bytes of four channels -> key pairs of each channel
+            const uint32_t a0 = __byte_perm(w[0][q4], w[1][q4], 0x5140), a1 = __byte_perm(w[0][q4], w[1][q4], 0x7362);
+            const uint32_t b0 = __byte_perm(w[2][q4], w[3][q4], 0x5140), b1 = __byte_perm(w[2][q4], w[3][q4], 0x7362);
+            mma16816(o[q4 * 4], pf[ks], e4m3x2_to_f16x2((uint16_t)(a0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b0 & 0xffffu)));
+            mma16816(o[q4 * 4 + 1], pf[ks], e4m3x2_to_f16x2((uint16_t)(a0 >> 16)), e4m3x2_to_f16x2((uint16_t)(b0 >> 16)));
+            mma16816(o[q4 * 4 + 2], pf[ks], e4m3x2_to_f16x2((uint16_t)(a1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b1 & 0xffffu)));
+            mma16816(o[q4 * 4 + 3], pf[ks], e4m3x2_to_f16x2((uint16_t)(a1 >> 16)), e4m3x2_to_f16x2((uint16_t)(b1 >> 16)));
+          }
+        }
+      }
+      __syncwarp();  // the stage is free
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // the warps' results, over their rings
+    {
+      float* mo = (float*)mine;
+      float2* ml = (float2*)(mine + ROWS * D * 4);
+#pragma unroll
+      for (int u = 0; u < (UP ? 2 : 1); ++u) {
+        float l = l_run[u];
+        l += __shfl_xor_sync(~0u, l, 1);
+        l += __shfl_xor_sync(~0u, l, 2);
+        if (ft == 0) ml[fg + 8 * u] = make_float2(m_run[u], l);
+        // channels (D/8) fg' of column n = 2 ft, 2 ft + 1
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < D / 8; j += 4)
+            *(float4*)(mo + (fg + 8 * u) * D + (D / 8) * (2 * ft + i) + j) =
+                make_float4(o[j][2 * u + i], o[j + 1][2 * u + i], o[j + 2][2 * u + i], o[j + 3][2 * u + i]);
+      }
+    }
+    __syncthreads();
+    const bool complete = k0 == 0 && k1 == sp.tiles;
+    const int slot = blockIdx.x * 2 + (k0 == 0 ? 1 : 0);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += THREADS) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float2 ml[WARPS];
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        ml[w] = ((const float2*)(smem + w * R::PER_WARP + ROWS * D * 4))[r];
+        m = fmaxf(m, ml[w].x);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float a = ml[w].x == -INFINITY && ml[w].y == 0.f ? 0.f : ex2(ml[w].x - (m == -INFINITY ? 0.f : m));
+        const float4 v = *(const float4*)(smem + w * R::PER_WARP + (r * D + c) * 4);
+        l += ml[w].y * a;
+        acc.x += v.x * a;
+        acc.y += v.y * a;
+        acc.z += v.z * a;
+        acc.w += v.w * a;
+      }
+      if (complete) {
+        const int tok = r / g.group;
+        const size_t at_o = (size_t)(sp.st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *(uint2*)(p.o + at_o * D + c) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (c == 0 && p.lse) p.lse[at_o] = (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
+      } else {
+        *(float4*)(slot_o(ws, D, slot) + r * D + c) = acc;
+        if (c == 0) slot_ml(ws, D, slot)[r] = make_float2(m, l);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the partial results of each (stream, head) that several thread blocks share.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const FwdParams p, void* ws) {
+  __shared__ long long part[8];
+  const Geom& g = p.g;
+  const int s = blockIdx.x / g.kv_heads, h = blockIdx.x % g.kv_heads;
+  // first tile of stream s = tiles of the streams before it
+  long long before = 0, total = 0;
+  {
+    const int t = threadIdx.x;
+    long long mine = 0, all = 0;
+    for (int i = t; i < g.streams; i += 128) {
+      const int n = stream_tiles(p, i).tiles;
+      all += n;
+      if (i < s) mine += n;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      mine += __shfl_xor_sync(~0u, mine, o);
+      all += __shfl_xor_sync(~0u, all, o);
+    }
+    if ((t & 31) == 0) {
+      part[t >> 5] = mine;
+      part[4 + (t >> 5)] = all;
+    }
+    __syncthreads();
+    before = (part[0] + part[1] + part[2] + part[3]) * g.kv_heads;
+    total = (part[4] + part[5] + part[6] + part[7]) * g.kv_heads;
+  }
+  const StreamTiles sp = stream_tiles(p, s);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (sp.tiles == 0) return;
+  const long long t0 = before + (long long)h * sp.tiles, t1 = t0 + sp.tiles - 1;
+  const int share = sharers(total);
+  const int c0 = (int)(((t0 + 1) * share - 1) / total), c1 = (int)(((t1 + 1) * share - 1) / total);
+  if (c0 == c1) return;
+  const int rows = sp.st.n * g.group;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = c0; b <= c1; ++b) {
+      const int slot = b * 2 + (b == c0 ? 1 : 0);
+      const float2 ml = __ldcg(slot_ml(ws, D, slot) + r);
+      const float4 v = __ldcg((const float4*)(slot_o(ws, D, slot) + r * D + c));
+      const float m_new = fmaxf(m, ml.x), ref = m_new == -INFINITY ? 0.f : m_new;
+      const float a = ex2(m - ref), e = ex2(ml.x - ref);
+      l = l * a + ml.y * e;
+      acc.x = acc.x * a + v.x * e;
+      acc.y = acc.y * a + v.y * e;
+      acc.z = acc.z * a + v.z * e;
+      acc.w = acc.w * a + v.w * e;
+      m = m_new;
+    }
+    const int tok = r / g.group;
+    const size_t at_o = (size_t)(sp.st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *(uint2*)(p.o + at_o * D + c) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (c == 0 && p.lse) p.lse[at_o] = (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <int D>
+cudaError_t launch(const FwdParams& p, void* ws, cudaStream_t st) {
+  constexpr int smem = Ring<D>::TOTAL;
+  const bool up = p.max_new * p.g.group > 8;
+  auto kernel = up ? few_kernel<D, true> : few_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<GRID, THREADS, smem, st>>>(p, ws);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.g.streams * p.g.kv_heads));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, ws);
+}
+
+}  // namespace few
+}  // namespace cache
+
+bool cache_few_fits(const cache::Geom& g, long long max_new) { return max_new * g.group <= cache::few::ROWS; }
+size_t cache_few_workspace(const cache::Geom& g) { return cache::few::workspace_bytes(g.d); }
+cudaError_t launch_cache_few(const cache::FwdParams& p, void* ws, cudaStream_t st) {
+  return p.g.d == 128 ? cache::few::launch<128>(p, ws, st) : cache::few::launch<64>(p, ws, st);
+}
+
+}  // namespace vattn
