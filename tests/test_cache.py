@@ -122,11 +122,11 @@ class FakeTensor:
     def element_size(self):
         return 1
 
-    def stride(self, i):
-        return self.stride_[i]
+    def stride(self):
+        return tuple(self.stride_)
 
     def get_device(self):
-        return self.device_
+        return self.device_ if self.is_cuda else -1
 
 
 class FakeLib:
@@ -144,7 +144,7 @@ class FakeLib:
 def B(monkeypatch):
     import video_dit_local_b200.binding as B
     monkeypatch.setattr(B, "lib", FakeLib())
-    monkeypatch.setattr(B, "_stream", lambda s: None)
+    monkeypatch.setattr(B, "_current_stream", lambda s, dev: None)
     return B
 
 
@@ -181,9 +181,13 @@ def test_wrappers_refuse_wrong_tensors(B, monkeypatch):
         B.vattn_cache_append(g, t(**kv, stride=[128, 1, 2]), t(**kv), t((5,)), t(), t(), t(), t())
     with pytest.raises(ValueError, match="slots"):
         B.vattn_cache_append(g, t(**kv), t(**kv), t((4,)), t(), t(), t(), t())
-    with pytest.raises(ValueError, match="current device"):
+    with pytest.raises(ValueError, match="another device"):
         B.vattn_cache_append(g, t(**kv), t(**kv, device=1), t((5,)), t(), t(), t(), t())
-    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    with pytest.raises(ValueError, match="current device"):
+        B.vattn_cache_append(g, t(**kv), t(**kv), t((5,)), t(), t(device=1), t(), t())
+    with pytest.raises(ValueError, match="host tensor"):
+        B.vattn_cache_plan(g, t(), t(), t(), t(cuda=False), *(t() for _ in range(6)))
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         B.vattn_cache_fwd(g, t((5, 4, 64)), *(t() for _ in range(7)), 0.1, 3, t())

@@ -679,3 +679,21 @@ def test_a_captured_step_is_replayed():
         s.check(new)
     del graph
     _status_ok(s.V)
+
+
+def test_bounded_waits_run_out():
+    """The load warp's first arrival withheld: the kernel gives up, reports it
+    and leaves the device usable."""
+    V = _v()
+    f = Fwd(d=128, kv_heads=1, group=2, pt=64, steps=[(400, 200)], seed=15)
+    want = f.run()
+    o, lse, ws = f.outputs()
+    V.vattn_debug_set(V.binding.VATTN_DEBUG_SKIP_ARRIVAL, 20_000_000)
+    try:
+        f.call(o, lse, ws)
+        assert V.vattn_get_status() == V.binding.VATTN_ERR_DEVICE_TIMEOUT
+    finally:
+        V.vattn_debug_set(0, 0)
+    assert (o[f.n:] == 7.5).all()
+    got = f.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

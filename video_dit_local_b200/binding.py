@@ -366,47 +366,71 @@ def vattn_workspace_size(op: int, geom: Geom) -> int:
     return n.value
 
 
-def _tokens(x, what: str):
-    """(address, token stride, tokens) of a [tokens, heads, d] CUDA tensor whose
-    tokens' rows are dense (a slice of a fused projection along dim 1 is)."""
-    if not x.is_cuda:
-        raise ValueError(f"{what} got a host tensor: pass a CUDA tensor")
-    n, heads, d = x.shape
-    if x.stride(2) != 1 or x.stride(1) != d:
-        raise ValueError(f"{what}: heads and channels of a token must be contiguous")
-    return x.data_ptr(), x.stride(0) if n > 1 else heads * d, n
-
-
-def _same_device(*tensors) -> None:
-    """The kernels run on the current device's stream: every tensor must live there."""
-    devices = {x.get_device() for x in tensors if x is not None and not isinstance(x, int)}
-    if not devices:
-        return
+# The cache calls are short enough for their argument checks to matter, so each
+# tensor is looked at once.
+def _device(x) -> int:
+    """The device of a call's first tensor; it must be the current one, on whose stream the kernels run."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("a device pointer argument got a host tensor: pass a CUDA tensor")
     import torch
-    if len(devices) > 1 or (torch.cuda.is_available() and devices != {torch.cuda.current_device()}):
-        raise ValueError(f"tensors on devices {sorted(devices)}: all must be on the current device")
+    if torch.cuda.is_initialized() and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {dev}: all must be on the current device")
+    return dev
+
+
+def _on(x, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor on device `dev`; None and raw addresses pass."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.get_device() != dev:
+        raise ValueError("a device pointer argument got a host tensor: pass a CUDA tensor" if x.get_device() < 0 else
+                         f"tensors on devices {dev} and {x.get_device()}: all must be on the current device")
+    if not x.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous (the library reads them as dense arrays)")
+    return x.data_ptr()
+
+
+def _tokens(x, what: str, dev: int):
+    """(address, token stride, tokens) of a [tokens, heads, d] tensor whose tokens'
+    rows are dense (a slice of a fused projection along dim 1 is)."""
+    if x.get_device() != dev:
+        raise ValueError(f"{what} is on another device than the call's other tensors")
+    n, heads, d = x.shape
+    token, head, channel = x.stride()
+    if channel != 1 or head != d:
+        raise ValueError(f"{what}: heads and channels of a token must be contiguous")
+    return x.data_ptr(), token if n > 1 else heads * d, n
+
+
+def _current_stream(stream, dev: int) -> int:
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def vattn_cache_plan(geom: CacheGeom, new_tokens, kv_lens, block_table, free_pages, n_free, kv_lens_out, n_free_out,
                      q_starts, slots, result, max_tokens: Optional[int] = None, stream=None) -> None:
     """Pages and slots of one step's new tokens (int32 tensors; max_tokens defaults to the length of slots)."""
-    _same_device(new_tokens, kv_lens, block_table, free_pages, n_free, kv_lens_out, n_free_out, q_starts, slots,
-                 result)
-    _check(lib.vattn_cache_plan(ctypes.byref(geom), _ptr(new_tokens), _ptr(kv_lens), _ptr(block_table),
-                                _ptr(free_pages), _ptr(n_free), _ptr(kv_lens_out), _ptr(n_free_out), _ptr(q_starts),
-                                _ptr(slots), slots.numel() if max_tokens is None else max_tokens, _ptr(result),
-                                _stream(stream)))
+    dev = -1 if isinstance(new_tokens, int) else _device(new_tokens)
+    _check(lib.vattn_cache_plan(ctypes.byref(geom), _on(new_tokens, dev), _on(kv_lens, dev), _on(block_table, dev),
+                                _on(free_pages, dev), _on(n_free, dev), _on(kv_lens_out, dev), _on(n_free_out, dev),
+                                _on(q_starts, dev), _on(slots, dev),
+                                slots.numel() if max_tokens is None else max_tokens, _on(result, dev),
+                                _current_stream(stream, dev)))
 
 
 def vattn_cache_append(geom: CacheGeom, k, v, slots, kcache, vcache, kscale, vscale, stream=None) -> None:
     """Quantise k, v [tokens, kv_heads, d] (bf16, may be slices of a fused projection) into their slots."""
-    _same_device(k, v, slots, kcache, vcache, kscale, vscale)
-    kp, ks, n = _tokens(k, "k")
-    vp, vs, nv = _tokens(v, "v")
+    dev = _device(k)
+    kp, ks, n = _tokens(k, "k", dev)
+    vp, vs, nv = _tokens(v, "v", dev)
     if nv != n or slots.numel() < n:
         raise ValueError(f"{n} keys, {nv} values and {slots.numel()} slots")
-    _check(lib.vattn_cache_append(ctypes.byref(geom), kp, ks, vp, vs, _ptr(slots), n, _ptr(kcache), _ptr(vcache),
-                                  _ptr(kscale), _ptr(vscale), _stream(stream)))
+    _check(lib.vattn_cache_append(ctypes.byref(geom), kp, ks, vp, vs, _on(slots, dev), n, _on(kcache, dev),
+                                  _on(vcache, dev), _on(kscale, dev), _on(vscale, dev),
+                                  _current_stream(stream, dev)))
 
 
 def vattn_cache_workspace_size(geom: CacheGeom, n_tokens: int, max_new: int) -> int:
@@ -418,13 +442,14 @@ def vattn_cache_workspace_size(geom: CacheGeom, n_tokens: int, max_new: int) -> 
 def vattn_cache_fwd(geom: CacheGeom, q, q_starts, kv_lens, block_table, kcache, vcache, kscale, vscale, scale: float,
                     max_new: int, o, lse=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
     """Attention of q [tokens, q_heads, d] (bf16, may be a slice of a fused projection) over the cache."""
-    _same_device(q, q_starts, kv_lens, block_table, kcache, vcache, kscale, vscale, o, lse, workspace)
+    dev = _device(q)
     if workspace is not None and not ws_bytes:
         ws_bytes = workspace.numel() * workspace.element_size()
-    qp, stride, n = _tokens(q, "q")
-    _check(lib.vattn_cache_fwd(ctypes.byref(geom), qp, stride, _ptr(q_starts), _ptr(kv_lens), _ptr(block_table),
-                               _ptr(kcache), _ptr(vcache), _ptr(kscale), _ptr(vscale), scale, n, max_new, _ptr(o),
-                               _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+    qp, stride, n = _tokens(q, "q", dev)
+    _check(lib.vattn_cache_fwd(ctypes.byref(geom), qp, stride, _on(q_starts, dev), _on(kv_lens, dev),
+                               _on(block_table, dev), _on(kcache, dev), _on(vcache, dev), _on(kscale, dev),
+                               _on(vscale, dev), scale, n, max_new, _on(o, dev), _on(lse, dev), _on(workspace, dev),
+                               ws_bytes, _current_stream(stream, dev)))
 
 
 def vattn_get_status(stream=None) -> int:

@@ -128,8 +128,12 @@ bool cache_few_fits(const cache::Geom& g, long long max_new);
 size_t cache_few_workspace(const cache::Geom& g);
 cudaError_t launch_cache_few(const cache::FwdParams& p, void* workspace, cudaStream_t st);
 
-// -- cache_attn.cu --
-size_t cache_fwd_workspace(const cache::Geom& g, long long n_tokens, long long max_new);
-cudaError_t launch_cache_fwd(const cache::FwdParams& p, void* workspace, cudaStream_t st);
+// -- cache_attn_many.cu --
+size_t cache_many_workspace(const cache::Geom& g, long long max_new);
+cudaError_t launch_cache_many(const cache::FwdParams& p, void* workspace, cudaStream_t st);
+
+// 3-D map over e4m3 cache pages [pages * kv_heads][page_tokens][d]: box = one
+// page of one kv head, 128-byte swizzle (64-byte at d = 64).
+bool make_tmap_pages(CUtensorMap* map, const void* base, int d, int page_tokens, long long heads, const char** err);
 
 }  // namespace vattn

@@ -61,6 +61,8 @@ int build_geom(const vattn_cache_geom* in, cache::Geom* g) {
   if (in->q_heads > 65535 || in->streams > 65535)
     return fail(VATTN_ERR_UNSUPPORTED, "q_heads and streams must be <= 65535");
   if (in->pages >= (1ll << 31) / pt) return fail(VATTN_ERR_UNSUPPORTED, "pages * page_tokens must be < 2^31");
+  if (in->pages * in->kv_heads >= (1ll << 31))
+    return fail(VATTN_ERR_UNSUPPORTED, "pages * kv_heads must be < 2^31");
   if ((long long)in->table_width * pt >= (1ll << 31))
     return fail(VATTN_ERR_UNSUPPORTED, "table_width * page_tokens must be < 2^31");
   g->streams = (int)in->streams;
@@ -89,6 +91,11 @@ int check_stride(const char* name, int64_t stride, int64_t heads, int64_t d) {
                 (long long)(heads * d));
   if (stride % 8) return fail(VATTN_ERR_ALIGN, "%s %lld is not a multiple of 8 elements", name, (long long)stride);
   return VATTN_OK;
+}
+
+size_t fwd_workspace(const cache::Geom& g, int64_t max_new) {
+  if (g.streams == 0 || max_new == 0) return 0;
+  return cache_few_fits(g, max_new) ? cache_few_workspace(g) : cache_many_workspace(g, max_new);
 }
 
 }  // namespace
@@ -173,7 +180,7 @@ int vattn_cache_workspace_size(const vattn_cache_geom* geom, int64_t n_tokens, i
   if ((r = check_tokens(n_tokens))) return r;
   if (max_new < 0) return fail(VATTN_ERR_INVALID_ARG, "max_new must be >= 0");
   if (!bytes) return fail(VATTN_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = cache_fwd_workspace(g, n_tokens, max_new < n_tokens ? max_new : n_tokens);
+  *bytes = fwd_workspace(g, max_new < n_tokens ? max_new : n_tokens);
   return ok();
 }
 
@@ -200,7 +207,7 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   REQUIRE_PTR(vscale);
   REQUIRE_PTR(o);
   if (lse && !aligned16(lse)) return fail(VATTN_ERR_ALIGN, "lse is not 16-byte aligned");
-  const size_t need = cache_fwd_workspace(g, n_tokens, max_new);
+  const size_t need = fwd_workspace(g, max_new);
   if (need > 0) {
     if (!workspace || ws_bytes < need)
       return fail(VATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
@@ -223,7 +230,10 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   p.o = (__nv_bfloat16*)o;
   p.lse = lse;
   p.ctl = current_ctl();
-  CHECK_LAUNCH(launch_cache_fwd(p, workspace, (cudaStream_t)stream), "cache_fwd launch");
+  if (cache_few_fits(g, max_new))
+    CHECK_LAUNCH(launch_cache_few(p, workspace, (cudaStream_t)stream), "cache_fwd launch");
+  else
+    CHECK_LAUNCH(launch_cache_many(p, workspace, (cudaStream_t)stream), "cache_fwd launch");
   return ok();
 }
 

@@ -1,0 +1,641 @@
+// Attention over the 8-bit key/value cache for many query rows (whole latent
+// frames): bound by the tensor pipe and the softmax, on tcgen05.
+//
+// A thread block takes 128 query rows (token, query head of the group) of one
+// stream and kv head and streams the keys they see in blocks of 128.  12 warps:
+//   warps 0-3 and 4-7  two softmax groups on alternate key blocks, each with an
+//                      S and an O accumulator in TMEM, joined at the end;
+//   warps 8, 9         bring V: bytes from the cache pages through registers,
+//                      e4m3 -> f16, into the swizzled tiles that P V reads;
+//   warp 10            K pages by TMA, and the blocks' scales;
+//   warp 11            issues the MMAs and owns the TMEM allocation.
+//
+// Q K^T runs on the cached bytes as they are (kind::f8f6f4).  A bf16 query has
+// 8 significant bits, an e4m3 value 4: each row is scaled by a power of two
+// into [128, 256) and split into two e4m3 values, hi + lo, whose products with
+// K add up in the same accumulator.  hi + lo is exact down to the e4m3 step
+// 2^-9, that is to 2^-17 of the row's largest element, and the two fp8 passes
+// cost what one bf16 pass would, without converting a key.  P V runs on f16: P
+// keeps 11 bits and V, converted exactly, is the part whose rows past a
+// stream's end must be zeroed anyway.
+//
+// Scales are powers of two per 16 keys: K's enters the factor of those 16
+// scores; V's the exponent of P, x_j = s_j + log2(vs), with the row sum taking
+// P 2^-log2(vs).  The reference m of a row moves only when its maximum grows by
+// more than 2^8 (then O is rescaled); P = 2^(x - m + 7) <= 2^15 in f16.
+#include <algorithm>
+
+#include "cache.cuh"
+#include "fwd_common.cuh"
+
+namespace vattn {
+namespace cache {
+namespace many {
+
+using fwd::idesc_e4m3_f32;
+using fwd::mma_ss_e4m3;
+
+constexpr int BM = 128, BN = 128;
+constexpr int THREADS = 384;
+constexpr int WARP_V = 8, V_WARPS = 2, WARP_K = 10, WARP_MMA = 11;
+constexpr int NK = 3;   // K ring stages
+constexpr int NV = 2;   // V ring stages
+// Scale ring: block j + 8 is written after Q K^T of block j + 5 is done, which
+// is issued after P of block j + 2, whose group has long read block j's slot.
+constexpr int NS = 8;
+constexpr float RESCALE = 8.0f;
+constexpr float P_SHIFT = 7.0f;
+constexpr int SUBS = BN / SCALE_TOKENS;
+
+template <int D>
+struct Smem {
+  static constexpr int QK = 128 * D;            // 128 rows of bytes
+  static constexpr int V = 128 * D * 2;         // 128 rows of f16
+  static constexpr int OFF_Q = 0;               // hi, lo
+  static constexpr int OFF_K = 2 * QK;
+  static constexpr int OFF_V = OFF_K + NK * QK;
+  static constexpr int OFF_SC = OFF_V + NV * V;              // NS x (8 K, 8 V) scales
+  static constexpr int OFF_XCH = OFF_SC + NS * 2 * SUBS * 4;
+  static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
+  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 2 + 1 + NS;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int TOTAL = OFF_MISC + 16;
+  static constexpr int ALLOC = TOTAL + 1024;
+};
+
+struct Params {
+  FwdParams f;
+  int q_tiles;   // tiles of 128 rows that a stream can have
+  int splits;    // thread blocks that share a tile's keys
+  float* part;   // splits > 1: partial results [stream][kv head][tile][split][128][d], then (m, l) pairs
+  float2* part_ml;
+};
+
+// Instruction descriptor, kind::f16, f16 x f16 -> f32, B MN-major (V rows are keys).
+constexpr uint32_t idesc_f16_pv(int N) {
+  return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+// K-major byte rows: 128-byte swizzle at d = 128, 64-byte at d = 64.
+template <int D>
+__device__ __forceinline__ uint64_t desc_bytes(uint32_t start) {
+  if (D == 128) return smem_desc_sw128(start, 16, 1024);
+  return (smem_desc_sw128(start, 16, 512) & ~(7ull << 61)) | (4ull << 61);
+}
+// 16-byte chunk c of byte row r in those layouts.
+template <int D>
+__device__ __forceinline__ uint32_t byte_chunk(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The keys of a tile of rows: blocks [first, first + count) of 128, those of
+// the tokens [lo, hi).
+struct TileKeys {
+  int lo, hi, first, count;
+};
+__device__ __forceinline__ TileKeys tile_keys(const Geom& g, const StreamStep& st, int row0, int rows) {
+  TileKeys t;
+  int x;
+  key_range(g, st, row0 / g.group, &t.lo, &x);
+  key_range(g, st, (row0 + rows - 1) / g.group, &x, &t.hi);
+  t.hi = max(t.hi, t.lo);
+  t.first = t.lo / BN;
+  t.count = t.hi > t.lo ? (t.hi + BN - 1) / BN - t.first : 0;
+  return t;
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant__ CUtensorMap tm_k, const Params pp) {
+  using L = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const FwdParams& p = pp.f;
+  const Geom& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // what this block computes; later tiles see more keys under a causal mask, so they go first
+  const int split = blockIdx.x % pp.splits;
+  const int tile = pp.q_tiles - 1 - blockIdx.x / pp.splits;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const StreamStep st = stream_step(p, s);
+  const int row0 = tile * BM;
+  const int rows = min(BM, st.n * g.group - row0);
+  if (rows <= 0) return;
+  const TileKeys tk = tile_keys(g, st, row0, rows);
+  const int b0 = tk.first + (int)((long long)tk.count * split / pp.splits);
+  const int nblk = tk.first + (int)((long long)tk.count * (split + 1) / pp.splits) - b0;
+  if (nblk == 0) {
+    // no keys here: rows that see none at all are written by the first split, the join skips the rest
+    if (tk.count == 0 && split == 0) {
+      for (int i = threadIdx.x; i < rows * (D / 8); i += THREADS) {
+        const int r = row0 + i / (D / 8), tok = r / g.group;
+        const size_t at = (size_t)(st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+        *(uint4*)(p.o + at * D + (i % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
+        if (i % (D / 8) == 0 && p.lse) p.lse[at] = -INFINITY;
+      }
+    }
+    return;
+  }
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* qk_done = k_full + NK;  // S_j in TMEM and K stage j % NK free
+  uint64_t* v_full = qk_done + NK;
+  uint64_t* v_empty = v_full + NV;
+  uint64_t* p_full = v_empty + NV;
+  uint64_t* o_final = p_full + 2;
+  uint64_t* sc_full = o_final + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  float2* xch = reinterpret_cast<float2*>(smem + L::OFF_XCH);
+  float* scales = reinterpret_cast<float*>(smem + L::OFF_SC);
+  WaitCtx wc;
+  wc.abort_flag = abort_flag;
+  wc.timeout_ns = p.ctl.timeout_ns;
+  wc.err_word = p.ctl.err_word;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 256);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&qk_done[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], V_WARPS);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 4);
+    mbar_init(o_final, 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&sc_full[i], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == WARP_K && lane == 0) tma_prefetch_desc(&tm_k);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int* table = p.table + (long long)s * g.width;
+  // Page of the 16 keys from `key` on; -1: none of them is to be read.
+  auto page_at = [&](int key) {
+    if (key >= tk.hi || key + SCALE_TOKENS <= tk.lo) return -1;
+    const int pg = __ldg(table + (key >> g.page_shift));
+    if ((unsigned)pg >= (unsigned)g.pages) {
+      report_error(p.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
+      return -1;
+    }
+    return pg;
+  };
+
+  if (warp == WARP_K) {
+    // Lanes 0-7 follow K's scales and pages, lanes 8-15 V's scales, one lane
+    // for 16 keys; pages are fetched two blocks ahead and scales one, so that
+    // the dependent loads do not stand in a row.
+    const int sub = lane & 7;
+    const float* sp = lane < 8 ? p.ks : p.vs;
+    auto page_of = [&](int j) { return j < nblk && lane < 16 ? page_at((b0 + j) * BN + sub * SCALE_TOKENS) : -1; };
+    auto scale_of = [&](int j, int pg) {
+      return pg < 0 ? 0.f
+                    : __ldg(sp + (cache_row(g, pg, h, ((b0 + j) * BN + sub * SCALE_TOKENS) & (g.page_tokens - 1)) >> 4));
+    };
+    int pg = page_of(0), pg_next = page_of(1);
+    float sc = scale_of(0, pg);
+    const int lanes_per_page = g.page_tokens >> 4;
+    int issued = 0;
+    bool ok = true;
+    for (int j = 0; j < nblk; ++j) {
+      const int pg_after = page_of(j + 2);
+      const float sc_next = scale_of(j + 1, pg_next);
+      const int sg = j % NK;
+      ok = __all_sync(~0u, mbar_wait(&qk_done[sg], ((j / NK) & 1) ^ 1, wc));
+      if (!ok || (p.ctl.debug_flags & VATTN_DEBUG_SKIP_ARRIVAL)) break;
+      // one box of page_tokens rows for each page that holds a key to be read
+      // (its first 16 keys may lie before the window: any of its groups of 16 names it)
+      int page = pg;
+      for (int i = 1; i < lanes_per_page; ++i) page = max(page, __shfl_down_sync(~0u, pg, i));
+      const bool want = lane < 8 && lane % lanes_per_page == 0 && page >= 0;
+      const uint32_t wanted = __ballot_sync(~0u, want);
+      if (lane == 0) mbar_arrive_expect_tx(&k_full[sg], __popc(wanted) * g.page_tokens * D);
+      __syncwarp();
+      if (want)
+        tma_load_3d(smem + L::OFF_K + sg * L::QK + lane * SCALE_TOKENS * D, &tm_k, &k_full[sg], 0, 0,
+                    page * g.kv_heads + h);
+      ++issued;
+      if (lane < 16) scales[(j % NS) * 2 * SUBS + lane] = sc;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc_full[j % NS]);
+      pg = pg_next;
+      pg_next = pg_after;
+      sc = sc_next;
+    }
+    if (lane == 0)  // every issued copy has landed before the block can exit (a no-op unless aborted)
+      for (int j = max(issued - NK, 0); j < issued; ++j) mbar_wait_drain(&k_full[j % NK], (j / NK) & 1, wc);
+  } else if (warp >= WARP_V && warp < WARP_V + V_WARPS) {
+    constexpr int CH = D / 16;                       // 16-byte chunks of a V row
+    constexpr int RP = 32 / CH;                      // rows of a warp-wide load
+    constexpr int NL = BN / V_WARPS / RP;            // loads of a block
+    constexpr int GROUPS = BN / V_WARPS / SCALE_TOKENS;
+    const int half = (warp - WARP_V) * (BN / V_WARPS);
+    const int c = lane % CH, r0 = lane / CH;
+    auto pages_of = [&](int j) {  // lane i < GROUPS: page of the warp's i-th 16 rows of block j
+      return j < nblk && lane < GROUPS ? page_at((b0 + j) * BN + half + lane * SCALE_TOKENS) : -1;
+    };
+    uint4 x[NL];
+    auto fetch = [&](int j, int i, int pages) {
+      const int r = half + i * RP + r0;
+      const int pg = __shfl_sync(~0u, pages, i * RP / SCALE_TOKENS);
+      const int key = (b0 + j) * BN + r;
+      // rows outside the keys read become zeros: P is 0 there, and what a page holds past a stream's end may be NaN
+      x[i] = pg >= 0 && key >= tk.lo && key < tk.hi
+                 ? __ldg((const uint4*)(p.vc + cache_row(g, pg, h, key & (g.page_tokens - 1)) * D) + c)
+                 : make_uint4(0, 0, 0, 0);
+    };
+    int pages = pages_of(0);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) fetch(0, i, pages);
+    pages = pages_of(1);
+    for (int j = 0; j < nblk; ++j) {
+      const int sg = j % NV;
+      const int pages_next = pages_of(j + 2);
+      if (!__all_sync(~0u, mbar_wait(&v_empty[sg], ((j / NV) & 1) ^ 1, wc))) break;
+      uint8_t* dst = smem + L::OFF_V + sg * L::V;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int r = half + i * RP + r0;
+        const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t out[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          out[2 * u] = e4m3x2_to_f16x2((uint16_t)(in[u] & 0xffffu));
+          out[2 * u + 1] = e4m3x2_to_f16x2((uint16_t)(in[u] >> 16));
+        }
+        // 16 channels: two 16-byte chunks of the row's 128-byte box; chunks 4..7 start with their
+        // second, so that eight lanes meet all banks
+        uint8_t* row = dst + (c >> 2) * (128 * 128) + r * 128;
+        const int first = 2 * (c & 3) + (c >> 2);
+        const uint4 v0 = make_uint4(out[0], out[1], out[2], out[3]), v1 = make_uint4(out[4], out[5], out[6], out[7]);
+        *(uint4*)(row + ((first ^ (r & 7)) << 4)) = c >> 2 ? v1 : v0;
+        *(uint4*)(row + (((first ^ 1) ^ (r & 7)) << 4)) = c >> 2 ? v0 : v1;
+        if (j + 1 < nblk) fetch(j + 1, i, pages);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[sg]);
+      pages = pages_next;
+    }
+  } else if (warp == WARP_MMA) {
+    if (lane == 0) {
+      const uint32_t q_base = smem_u32(smem + L::OFF_Q);
+      const uint32_t k_base = smem_u32(smem + L::OFF_K);
+      const uint32_t v_base = smem_u32(smem + L::OFF_V);
+      bool ok = mbar_wait(q_full, 0, wc);
+      auto issue_qk = [&](int j) -> bool {
+        const int sg = j % NK;
+        if (!mbar_wait(&k_full[sg], (j / NK) & 1, wc)) return false;
+        tc_fence_after();
+        const uint32_t kb = k_base + sg * L::QK;
+        const uint32_t d_tmem = tmem + (uint32_t)((j & 1) * 128);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)  // hi, lo
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_ss_e4m3(d_tmem, desc_bytes<D>(q_base + part * L::QK + kk * 32), desc_bytes<D>(kb + kk * 32),
+                        idesc_e4m3_f32(BM, BN), part + kk > 0);
+        tc_commit(&qk_done[sg]);
+        return true;
+      };
+      if (ok) ok = issue_qk(0);
+      if (ok && nblk > 1) ok = issue_qk(1);
+      for (int j = 0; ok && j < nblk; ++j) {
+        const int w = j & 1;
+        if (!mbar_wait(&p_full[w], (j >> 1) & 1, wc)) break;
+        const int sg = j % NV;
+        if (!mbar_wait(&v_full[sg], (j / NV) & 1, wc)) break;
+        tc_fence_after();
+        const uint32_t vb = v_base + sg * L::V;
+        const uint32_t o_tmem = tmem + 256 + (uint32_t)(w * 128);
+        const uint32_t p_tmem = tmem + (uint32_t)(w * 128);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(o_tmem, p_tmem + kk * 8, smem_desc_sw128(vb + kk * 2048, 128 * 128, 1024), idesc_f16_pv(D),
+                 (j >= 2 || kk > 0) ? 1u : 0u);
+        tc_commit(&v_empty[sg]);
+        if (j + 2 < nblk) ok = issue_qk(j + 2);
+      }
+      tc_commit(o_final);
+      // every MMA this thread issued must be finished before TMEM is freed
+      mbar_wait_drain(o_final, 0, wc);
+    }
+  } else {
+    // ---------------- softmax groups ----------------
+    const int w = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const bool real = row < rows;
+    const int tok = real ? (row0 + row) / g.group : 0;
+    const size_t out_row =
+        (size_t)(st.row0 + tok) * g.q_heads + h * g.group + (real ? row0 + row - tok * g.group : 0);
+    int lo = 0, hi = 0;
+    if (real) key_range(g, st, tok, &lo, &hi);
+    // half a query row a thread (the group's half): scaled, split into hi + lo, written in the MMA's layout
+    float c_row, poison;
+    {
+      constexpr int NC = D / 32;  // 16-element chunks of half a row
+      uint4 x[2 * NC];
+      uint32_t m = 0;
+      const uint4* src = (const uint4*)(p.q + (long long)(st.row0 + tok) * p.q_stride +
+                                        (long long)(h * g.group + (real ? row0 + row - tok * g.group : 0)) * D +
+                                        w * (D / 2));
+#pragma unroll
+      for (int i = 0; i < 2 * NC; ++i) {
+        x[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      xch[w * 128 + row].x = __uint_as_float(m);
+      named_bar_sync(1, 256);
+      m = max(m, __float_as_uint(xch[(1 - w) * 128 + row].x));
+      named_bar_sync(1, 256);
+      poison = m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
+      const int sh = m == 0 ? 0 : min(7 - ((int)(m >> 7) - 127), 126);
+      const float up = __int_as_float((sh + 127) << 23);
+      c_row = p.scale_log2 * __int_as_float((127 - sh) << 23);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        uint32_t hv[4], lv[4];
+        const uint32_t in[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
+                                x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t hh[2], ll[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = bf16lo(in[2 * u + e]) * up, b = bf16hi(in[2 * u + e]) * up;
+            hh[e] = pack_e4m3x2(a, b);
+            const float2 back = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)hh[e]));
+            ll[e] = pack_e4m3x2(a - back.x, b - back.y);
+          }
+          hv[u] = hh[0] | (hh[1] << 16);
+          lv[u] = ll[0] | (ll[1] << 16);
+        }
+        const uint32_t at = byte_chunk<D>(row, w * NC + i);
+        *(uint4*)(smem + L::OFF_Q + at) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        *(uint4*)(smem + L::OFF_Q + L::QK + at) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
+      }
+      fence_async_smem();
+      mbar_arrive(q_full);
+    }
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_addr + (uint32_t)(w * 128);
+    const uint32_t tO = tmem + lane_addr + 256u + (uint32_t)(w * 128);
+    float m_ref = -INFINITY, l_sum = 0.f;
+    int qs = w;        // qk_done stage of this group's next block ...
+    uint32_t qph = 0;  // ... and its phase parity
+    bool ok = true;
+    for (int i = 0;; ++i) {
+      const int j = 2 * i + w;
+      if (j >= nblk) break;
+      ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&qk_done[qs], qph, wc);
+      qs += 2;
+      if (qs >= NK) {
+        qs -= NK;
+        qph ^= 1u;
+      }
+      ok = __all_sync(~0u, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(tS + q4 * 32, sr[q4]);
+      const float* sc = scales + (j % NS) * 2 * SUBS;
+      float f[SUBS], e[SUBS];  // x = S f + e
+#pragma unroll
+      for (int b = 0; b < SUBS; ++b) {
+        f[b] = fmaxf(c_row * sc[b], 1.17549435e-38f);  // > 0: a masked score stays -inf
+        e[b] = (float)((__float_as_int(sc[SUBS + b]) >> 23) - 127) + poison;
+      }
+      tmem_wait_ld();
+      const int from = lo - (b0 + j) * BN, to = hi - (b0 + j) * BN;
+      if (from > 0 || to < BN) {
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (q4 * 32 + c < from || q4 * 32 + c >= to) sr[q4][c] = __float_as_uint(-INFINITY);
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < SUBS; ++b) {
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          const uint32_t* v = &sr[b >> 1][(b & 1) * 16 + c];
+          m0 = fmax3(m0, __uint_as_float(v[0]), __uint_as_float(v[1]));
+          m1 = fmax3(m1, __uint_as_float(v[2]), __uint_as_float(v[3]));
+        }
+        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), f[b], e[b]));
+      }
+      bool need = false;
+      float alpha = 1.f;
+      if (i == 0) {
+        m_ref = mx;
+      } else if (mx > m_ref + RESCALE) {
+        need = true;
+        alpha = ex2(m_ref - mx);
+        m_ref = mx;
+        l_sum *= alpha;
+      }
+      const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - P_SHIFT;
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int b2 = 0; b2 < 2; ++b2) {
+          const int b = q4 * 2 + b2;
+          const float2 ff = make_float2(f[b], f[b]), ee = make_float2(e[b] - ref, e[b] - ref);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t* v = &sr[q4][b2 * 16 + 2 * c];
+            const float2 x = ffma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), ff, ee);
+            const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+            sum = fadd2(sum, pr);
+            pk[b2 * 8 + c] = pack_f16(pr.x, pr.y);
+          }
+          // P 2^-log2(vs); an unused block's scale reads 0, exponent -127, with P = 0
+          const float inv = __int_as_float((254 << 23) - max(__float_as_int(sc[SUBS + b]) & 0x7f800000, 1 << 23));
+          l_sum = fmaf(sum.x + sum.y, inv, l_sum);
+        }
+        tmem_st16(tS + q4 * 16, pk);
+      }
+      if (__any_sync(~0u, need)) {
+        // O of this group is quiescent: the commit that signalled this S also
+        // covers the previous P V into it, and the next one waits for p_full.
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c0, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+          tmem_st32(tO + c0, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[w]);
+    }
+    // ---------------- epilogue ----------------
+    if (ok && !*abort_flag) ok = mbar_wait(o_final, 0, wc);
+    ok = __all_sync(~0u, ok);
+    tc_fence_after();
+    xch[w * 128 + row] = make_float2(m_ref, l_sum);
+    named_bar_sync(1, 256);
+    if (ok && !*abort_flag) {
+      const float2 other = xch[(1 - w) * 128 + row];
+      const float m = fmaxf(m_ref, other.x);
+      const float m0 = m == -INFINITY ? 0.f : m;
+      const float a_self = ex2(m_ref - m0), a_other = ex2(other.x - m0);
+      // a group without blocks has l = 0 and m = -inf
+      const float l = l_sum * a_self + other.y * a_other;
+      const bool whole = pp.splits == 1;
+      const float norm = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const float a0 = (w == 0 ? a_self : a_other) * norm;
+      const float a1 = (w == 0 ? a_other : a_self) * norm;
+      const bool have1 = nblk >= 2;
+      const uint32_t tO0 = tmem + lane_addr + 256u, tO1 = tmem + lane_addr + 384u;
+      const size_t pr = whole ? 0
+                              : ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + split) * BM + row;
+#pragma unroll
+      for (int c0 = (w * D) / 2; c0 < ((w + 1) * D) / 2; c0 += 32) {
+        uint32_t x0[32], x1[32];
+        tmem_ld32(tO0 + c0, x0);
+        if (have1) tmem_ld32(tO1 + c0, x1);
+        tmem_wait_ld();
+        float* o = reinterpret_cast<float*>(x0);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = o[c] * a0 + (have1 ? __uint_as_float(x1[c]) * a1 : 0.f);
+        if (real && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * D + c0);
+#pragma unroll
+          for (int v4 = 0; v4 < 4; ++v4)
+            dst[v4] = make_uint4(pack_bf16(o[8 * v4 + 0], o[8 * v4 + 1]), pack_bf16(o[8 * v4 + 2], o[8 * v4 + 3]),
+                                 pack_bf16(o[8 * v4 + 4], o[8 * v4 + 5]), pack_bf16(o[8 * v4 + 6], o[8 * v4 + 7]));
+        } else if (real) {
+          float4* dst = reinterpret_cast<float4*>(pp.part + pr * D + c0);
+#pragma unroll
+          for (int v4 = 0; v4 < 8; ++v4)
+            dst[v4] = make_float4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+        }
+      }
+      if (w == 0 && real) {
+        if (!whole)
+          pp.part_ml[pr] = make_float2(m, l);
+        else if (p.lse)
+          p.lse[out_row] = (m - P_SHIFT + __log2f(l)) * 0.69314718055994531f;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the splits of each row, in their order; one warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const Params pp) {
+  const FwdParams& p = pp.f;
+  const Geom& g = p.g;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const StreamStep st = stream_step(p, s);
+  const int all = st.n * g.group;
+  if (r >= all) return;
+  const int tile = r / BM, row = r % BM;
+  const TileKeys tk = tile_keys(g, st, tile * BM, min(BM, all - tile * BM));
+  if (tk.count == 0) return;
+  constexpr int PER = D / 32;
+  float acc[PER] = {};
+  float m = -INFINITY, l = 0.f;
+  for (int i = 0; i < pp.splits; ++i) {
+    if ((long long)tk.count * i / pp.splits == (long long)tk.count * (i + 1) / pp.splits) continue;
+    const size_t pr = ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + i) * BM + row;
+    const float2 ml = pp.part_ml[pr];
+    const float m_new = fmaxf(m, ml.x), ref = m_new == -INFINITY ? 0.f : m_new;
+    const float a = ex2(m - ref), e = ex2(ml.x - ref);
+    l = l * a + ml.y * e;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] = acc[c] * a + pp.part[pr * D + lane * PER + c] * e;
+    m = m_new;
+  }
+  const int tok = r / g.group;
+  const size_t at = (size_t)(st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int c = 0; c < PER; c += 2)
+    *(uint32_t*)(p.o + at * D + lane * PER + c) = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[at] = (m - P_SHIFT + __log2f(l)) * 0.69314718055994531f;
+}
+
+int tiles_of(const Geom& g, long long max_new) { return (int)((max_new * g.group + BM - 1) / BM); }
+
+// Thread blocks per tile of rows: enough to use the 148 SMs when there are few tiles.
+int splits_of(const Geom& g, long long max_new) {
+  const long long items = (long long)g.streams * g.kv_heads * tiles_of(g, max_new);
+  return items >= 148 ? 1 : (int)std::min<long long>(148 / items, 32);
+}
+size_t part_rows(const Geom& g, long long max_new) {
+  const int sp = splits_of(g, max_new);
+  return sp == 1 ? 0 : (size_t)g.streams * g.kv_heads * tiles_of(g, max_new) * sp * BM;
+}
+
+template <int D>
+cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
+  Params p;
+  p.f = f;
+  p.q_tiles = tiles_of(f.g, f.max_new);
+  p.splits = splits_of(f.g, f.max_new);
+  p.part = (float*)ws;
+  p.part_ml = (float2*)(p.part + part_rows(f.g, f.max_new) * D);
+  CUtensorMap tk;
+  const char* err = nullptr;
+  if (!make_tmap_pages(&tk, f.kc, D, f.g.page_tokens, (long long)f.g.pages * f.g.kv_heads, &err))
+    return cudaErrorInvalidValue;
+  auto kernel = many_kernel<D>;
+  constexpr int smem = Smem<D>::ALLOC;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3(p.q_tiles * p.splits, f.g.kv_heads, f.g.streams), THREADS, smem, stream>>>(tk, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int rows = (int)(f.max_new * f.g.group);
+  join_kernel<D><<<dim3((rows + 7) / 8, f.g.kv_heads, f.g.streams), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace many
+}  // namespace cache
+
+size_t cache_many_workspace(const cache::Geom& g, long long max_new) {
+  return cache::many::part_rows(g, max_new) * (g.d + 2) * sizeof(float);
+}
+cudaError_t launch_cache_many(const cache::FwdParams& p, void* ws, cudaStream_t st) {
+  return p.g.d == 128 ? cache::many::launch<128>(p, ws, st) : cache::many::launch<64>(p, ws, st);
+}
+
+}  // namespace vattn

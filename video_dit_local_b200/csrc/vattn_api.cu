@@ -8,6 +8,7 @@
 #include <cstring>
 #include <string>
 
+#include "cache.cuh"
 #include "common.cuh"
 
 namespace vattn {
@@ -235,6 +236,28 @@ bool make_tmap_rows_u8(CUtensorMap* map, const void* base, int d, long long rows
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled failed";
+    return false;
+  }
+  return true;
+}
+
+// Pages of the 8-bit cache: [heads][page_tokens][d] bytes, box = one page of
+// one head, its rows swizzled by their own width.
+bool make_tmap_pages(CUtensorMap* map, const void* base, int d, int page_tokens, long long heads, const char** err) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) {
+    *err = "cuTensorMapEncodeTiled unavailable";
+    return false;
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page_tokens, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)page_tokens * d};
+  cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)page_tokens, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     *err = "cuTensorMapEncodeTiled failed";
     return false;
