@@ -5,9 +5,9 @@
 // stream and kv head and streams the keys they see in blocks of 128.  12 warps:
 //   warps 0-3 and 4-7  two softmax groups on alternate key blocks, each with an
 //                      S and an O accumulator in TMEM, joined at the end;
-//   warps 8, 9         bring V: bytes from the cache pages through registers,
-//                      e4m3 -> f16, into the swizzled tiles that P V reads;
-//   warp 10            K pages by TMA, and the blocks' scales;
+//   warps 8, 9         convert V, e4m3 -> f16, from one swizzled tile into the
+//                      other that P V reads;
+//   warp 10            K and V pages by TMA, and the blocks' scales;
 //   warp 11            issues the MMAs and owns the TMEM allocation.
 //
 // Q K^T runs on the cached bytes as they are (kind::f8f6f4).  A bf16 query has
@@ -38,8 +38,8 @@ using fwd::mma_ss_e4m3;
 constexpr int BM = 128, BN = 128;
 constexpr int THREADS = 384;
 constexpr int WARP_V = 8, V_WARPS = 2, WARP_K = 10, WARP_MMA = 11;
-constexpr int NK = 3;   // K ring stages
-constexpr int NV = 2;   // V ring stages
+constexpr int NK = 3;   // ring stages of K and of V's bytes
+constexpr int NV = 2;   // ring stages of V as f16
 // Scale ring: block j + 8 is written after Q K^T of block j + 5 is done, which
 // is issued after P of block j + 2, whose group has long read block j's slot.
 constexpr int NS = 8;
@@ -53,11 +53,12 @@ struct Smem {
   static constexpr int V = 128 * D * 2;         // 128 rows of f16
   static constexpr int OFF_Q = 0;               // hi, lo
   static constexpr int OFF_K = 2 * QK;
-  static constexpr int OFF_V = OFF_K + NK * QK;
+  static constexpr int OFF_V8 = OFF_K + NK * QK;  // V as cached, in step with K
+  static constexpr int OFF_V = OFF_V8 + NK * QK;
   static constexpr int OFF_SC = OFF_V + NV * V;              // NS x (8 K, 8 V) scales
   static constexpr int OFF_XCH = OFF_SC + NS * 2 * SUBS * 4;
   static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
-  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 2 + 1 + NS;
+  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 1 + NS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int TOTAL = OFF_MISC + 16;
   static constexpr int ALLOC = TOTAL + 1024;
@@ -110,7 +111,9 @@ __device__ __forceinline__ TileKeys tile_keys(const Geom& g, const StreamStep& s
 }
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant__ CUtensorMap tm_k, const Params pp) {
+__global__ void __launch_bounds__(THREADS, 1)
+    many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const Params pp) {
   using L = Smem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -144,9 +147,10 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_full = bars;
-  uint64_t* k_full = bars + 1;
-  uint64_t* qk_done = k_full + NK;  // S_j in TMEM and K stage j % NK free
-  uint64_t* v_full = qk_done + NK;
+  uint64_t* kv_full = bars + 1;      // K and V bytes of a stage have landed
+  uint64_t* qk_done = kv_full + NK;  // S_j in TMEM and K stage j % NK free
+  uint64_t* v8_empty = qk_done + NK; // V stage j % NK converted
+  uint64_t* v_full = v8_empty + NK;
   uint64_t* v_empty = v_full + NV;
   uint64_t* p_full = v_empty + NV;
   uint64_t* o_final = p_full + 2;
@@ -163,8 +167,9 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
   if (threadIdx.x == 0) {
     mbar_init(q_full, 256);
     for (int i = 0; i < NK; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&kv_full[i], 1);
       mbar_init(&qk_done[i], 1);
+      mbar_init(&v8_empty[i], V_WARPS);
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(&v_full[i], V_WARPS);
@@ -180,7 +185,10 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == WARP_K && lane == 0) tma_prefetch_desc(&tm_k);
+  if (warp == WARP_K && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -217,7 +225,8 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
       const int pg_after = page_of(j + 2);
       const float sc_next = scale_of(j + 1, pg_next);
       const int sg = j % NK;
-      ok = __all_sync(~0u, mbar_wait(&qk_done[sg], ((j / NK) & 1) ^ 1, wc));
+      const uint32_t free_phase = ((j / NK) & 1) ^ 1;
+      ok = __all_sync(~0u, mbar_wait(&qk_done[sg], free_phase, wc) && mbar_wait(&v8_empty[sg], free_phase, wc));
       if (!ok || (p.ctl.debug_flags & VATTN_DEBUG_SKIP_ARRIVAL)) break;
       // one box of page_tokens rows for each page that holds a key to be read
       // (its first 16 keys may lie before the window: any of its groups of 16 names it)
@@ -225,11 +234,13 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
       for (int i = 1; i < lanes_per_page; ++i) page = max(page, __shfl_down_sync(~0u, pg, i));
       const bool want = lane < 8 && lane % lanes_per_page == 0 && page >= 0;
       const uint32_t wanted = __ballot_sync(~0u, want);
-      if (lane == 0) mbar_arrive_expect_tx(&k_full[sg], __popc(wanted) * g.page_tokens * D);
+      if (lane == 0) mbar_arrive_expect_tx(&kv_full[sg], 2 * __popc(wanted) * g.page_tokens * D);
       __syncwarp();
-      if (want)
-        tma_load_3d(smem + L::OFF_K + sg * L::QK + lane * SCALE_TOKENS * D, &tm_k, &k_full[sg], 0, 0,
-                    page * g.kv_heads + h);
+      if (want) {
+        const int at = sg * L::QK + lane * SCALE_TOKENS * D;
+        tma_load_3d(smem + L::OFF_K + at, &tm_k, &kv_full[sg], 0, 0, page * g.kv_heads + h);
+        tma_load_3d(smem + L::OFF_V8 + at, &tm_v, &kv_full[sg], 0, 0, page * g.kv_heads + h);
+      }
       ++issued;
       if (lane < 16) scales[(j % NS) * 2 * SUBS + lane] = sc;
       __syncwarp();
@@ -239,59 +250,50 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
       sc = sc_next;
     }
     if (lane == 0)  // every issued copy has landed before the block can exit (a no-op unless aborted)
-      for (int j = max(issued - NK, 0); j < issued; ++j) mbar_wait_drain(&k_full[j % NK], (j / NK) & 1, wc);
+      for (int j = max(issued - NK, 0); j < issued; ++j) mbar_wait_drain(&kv_full[j % NK], (j / NK) & 1, wc);
   } else if (warp >= WARP_V && warp < WARP_V + V_WARPS) {
-    constexpr int CH = D / 16;                       // 16-byte chunks of a V row
-    constexpr int RP = 32 / CH;                      // rows of a warp-wide load
-    constexpr int NL = BN / V_WARPS / RP;            // loads of a block
-    constexpr int GROUPS = BN / V_WARPS / SCALE_TOKENS;
+    constexpr int RP = 512 / D;            // rows of a warp-wide read, 16 bytes a lane
+    constexpr int NL = BN / V_WARPS / RP;  // reads of a block
     const int half = (warp - WARP_V) * (BN / V_WARPS);
-    const int c = lane % CH, r0 = lane / CH;
-    auto pages_of = [&](int j) {  // lane i < GROUPS: page of the warp's i-th 16 rows of block j
-      return j < nblk && lane < GROUPS ? page_at((b0 + j) * BN + half + lane * SCALE_TOKENS) : -1;
+    // Eight lanes at a time read, and then store, four chunks of two rows.  d = 128: of rows r and r ^ 5, whose
+    // swizzles differ in bit 2 (so the reads meet all banks) and in bit 0 (so the stores do); d = 64: of rows r, r + 1.
+    const int c = D == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
+    auto row_of = [&](int i) {
+      return D == 128 ? half + 8 * (i >> 1) + ((2 * (i & 1) + (lane >> 4)) ^ (lane & 4 ? 5 : 0)) : half + i * RP + (lane >> 2);
     };
-    uint4 x[NL];
-    auto fetch = [&](int j, int i, int pages) {
-      const int r = half + i * RP + r0;
-      const int pg = __shfl_sync(~0u, pages, i * RP / SCALE_TOKENS);
-      const int key = (b0 + j) * BN + r;
-      // rows outside the keys read become zeros: P is 0 there, and what a page holds past a stream's end may be NaN
-      x[i] = pg >= 0 && key >= tk.lo && key < tk.hi
-                 ? __ldg((const uint4*)(p.vc + cache_row(g, pg, h, key & (g.page_tokens - 1)) * D) + c)
-                 : make_uint4(0, 0, 0, 0);
-    };
-    int pages = pages_of(0);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) fetch(0, i, pages);
-    pages = pages_of(1);
     for (int j = 0; j < nblk; ++j) {
-      const int sg = j % NV;
-      const int pages_next = pages_of(j + 2);
-      if (!__all_sync(~0u, mbar_wait(&v_empty[sg], ((j / NV) & 1) ^ 1, wc))) break;
-      uint8_t* dst = smem + L::OFF_V + sg * L::V;
-#pragma unroll
+      const int s8 = j % NK, sg = j % NV;
+      if (!__all_sync(~0u, mbar_wait(&kv_full[s8], (j / NK) & 1, wc) &&
+                               mbar_wait(&v_empty[sg], ((j / NV) & 1) ^ 1, wc)))
+        break;
+      const uint8_t* src = smem + L::OFF_V8 + s8 * L::QK;
+      uint8_t* dst = smem + L::OFF_V + sg * L::V + (c >> 2) * (128 * 128);
+      // rows outside the keys read become zeros: P is 0 there, and what a page holds past a stream's end may be NaN
+      const int from = tk.lo - (b0 + j) * BN, to = tk.hi - (b0 + j) * BN;
+      const bool all = from <= 0 && to >= BN;
+#pragma unroll 8
       for (int i = 0; i < NL; ++i) {
-        const int r = half + i * RP + r0;
-        const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const int r = row_of(i);
+        uint4 x = *(const uint4*)(src + byte_chunk<D>(r, c));
+        if (!all && (r < from || r >= to)) x = make_uint4(0, 0, 0, 0);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
         uint32_t out[8];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           out[2 * u] = e4m3x2_to_f16x2((uint16_t)(in[u] & 0xffffu));
           out[2 * u + 1] = e4m3x2_to_f16x2((uint16_t)(in[u] >> 16));
         }
-        // 16 channels: two 16-byte chunks of the row's 128-byte box; chunks 4..7 start with their
-        // second, so that eight lanes meet all banks
-        uint8_t* row = dst + (c >> 2) * (128 * 128) + r * 128;
-        const int first = 2 * (c & 3) + (c >> 2);
-        const uint4 v0 = make_uint4(out[0], out[1], out[2], out[3]), v1 = make_uint4(out[4], out[5], out[6], out[7]);
-        *(uint4*)(row + ((first ^ (r & 7)) << 4)) = c >> 2 ? v1 : v0;
-        *(uint4*)(row + (((first ^ 1) ^ (r & 7)) << 4)) = c >> 2 ? v0 : v1;
-        if (j + 1 < nblk) fetch(j + 1, i, pages);
+        // 16 channels: two 16-byte chunks of the row's 128-byte box
+        const int at = (2 * (c & 3)) ^ (r & 7);
+        *(uint4*)(dst + r * 128 + (at << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+        *(uint4*)(dst + r * 128 + ((at ^ 1) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[sg]);
-      pages = pages_next;
+      if (lane == 0) {
+        mbar_arrive(&v8_empty[s8]);
+        mbar_arrive(&v_full[sg]);
+      }
     }
   } else if (warp == WARP_MMA) {
     if (lane == 0) {
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1) many_kernel(const __grid_constant_
       bool ok = mbar_wait(q_full, 0, wc);
       auto issue_qk = [&](int j) -> bool {
         const int sg = j % NK;
-        if (!mbar_wait(&k_full[sg], (j / NK) & 1, wc)) return false;
+        if (!mbar_wait(&kv_full[sg], (j / NK) & 1, wc)) return false;
         tc_fence_after();
         const uint32_t kb = k_base + sg * L::QK;
         const uint32_t d_tmem = tmem + (uint32_t)((j & 1) * 128);
@@ -612,15 +614,17 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   p.splits = splits_of(f.g, f.max_new);
   p.part = (float*)ws;
   p.part_ml = (float2*)(p.part + part_rows(f.g, f.max_new) * D);
-  CUtensorMap tk;
+  CUtensorMap tk, tv;
   const char* err = nullptr;
-  if (!make_tmap_pages(&tk, f.kc, D, f.g.page_tokens, (long long)f.g.pages * f.g.kv_heads, &err))
+  const long long heads = (long long)f.g.pages * f.g.kv_heads;
+  if (!make_tmap_pages(&tk, f.kc, D, f.g.page_tokens, heads, &err) ||
+      !make_tmap_pages(&tv, f.vc, D, f.g.page_tokens, heads, &err))
     return cudaErrorInvalidValue;
   auto kernel = many_kernel<D>;
   constexpr int smem = Smem<D>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(p.q_tiles * p.splits, f.g.kv_heads, f.g.streams), THREADS, smem, stream>>>(tk, p);
+  kernel<<<dim3(p.q_tiles * p.splits, f.g.kv_heads, f.g.streams), THREADS, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   const int rows = (int)(f.max_new * f.g.group);
