@@ -1,10 +1,15 @@
 // Attention over the 8-bit key/value cache for many query rows (whole latent
 // frames): bound by the tensor pipe and the softmax, on tcgen05.
 //
-// A thread block takes 128 query rows (token, query head of the group) of one
-// stream and kv head and streams the keys they see in blocks of 128.  12 warps:
-//   warps 0-3 and 4-7  two softmax groups on alternate key blocks, each with an
-//                      S and an O accumulator in TMEM, joined at the end;
+// A thread block takes the query rows (token, query head of the group) of one
+// stream and kv head in tiles of 128 and streams the keys they see in blocks of
+// 128.  12 warps:
+//   warps 0-3 and 4-7  two softmax groups, each with an S and an O accumulator
+//                      in TMEM.  TWO = true: a tile of rows each (256 rows a
+//                      thread block), on the same key blocks, so that one
+//                      conversion of V serves 256 rows; false (no stream has
+//                      more than 128 rows): one tile, alternate key blocks,
+//                      joined at the end;
 //   warps 8, 9         convert V, e4m3 -> f16, from one swizzled tile into the
 //                      other that P V reads;
 //   warp 10            K and V pages by TMA, and the blocks' scales;
@@ -38,27 +43,29 @@ using fwd::mma_ss_e4m3;
 constexpr int BM = 128, BN = 128;
 constexpr int THREADS = 384;
 constexpr int WARP_V = 8, V_WARPS = 2, WARP_K = 10, WARP_MMA = 11;
-constexpr int NK = 3;   // ring stages of K and of V's bytes
 constexpr int NV = 2;   // ring stages of V as f16
-// Scale ring: block j + 8 is written after Q K^T of block j + 5 is done, which
-// is issued after P of block j + 2, whose group has long read block j's slot.
+// Scale ring: block j + 8 is written after Q K^T of block j + 5 (or j + 6) is
+// done, which is issued after P of block j + 2, whose group has long read block
+// j's slot.
 constexpr int NS = 8;
 constexpr float RESCALE = 8.0f;
 constexpr float P_SHIFT = 7.0f;
 constexpr int SUBS = BN / SCALE_TOKENS;
 
-template <int D>
+template <int D, bool TWO>
 struct Smem {
+  static constexpr int TILES = TWO ? 2 : 1;     // tiles of query rows
+  static constexpr int NK = TWO ? 2 : 3;        // ring stages of K and of V's bytes
   static constexpr int QK = 128 * D;            // 128 rows of bytes
   static constexpr int V = 128 * D * 2;         // 128 rows of f16
-  static constexpr int OFF_Q = 0;               // hi, lo
-  static constexpr int OFF_K = 2 * QK;
+  static constexpr int OFF_Q = 0;               // hi and lo of each tile
+  static constexpr int OFF_K = TILES * 2 * QK;
   static constexpr int OFF_V8 = OFF_K + NK * QK;  // V as cached, in step with K
   static constexpr int OFF_V = OFF_V8 + NK * QK;
   static constexpr int OFF_SC = OFF_V + NV * V;              // NS x (8 K, 8 V) scales
   static constexpr int OFF_XCH = OFF_SC + NS * 2 * SUBS * 4;
   static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
-  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 1 + NS;
+  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 1 + NS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int TOTAL = OFF_MISC + 16;
   static constexpr int ALLOC = TOTAL + 1024;
@@ -66,9 +73,9 @@ struct Smem {
 
 struct Params {
   FwdParams f;
-  int q_tiles;   // tiles of 128 rows that a stream can have
+  int q_tiles;   // tiles of rows (of all of a thread block's) that a stream can have
   int splits;    // thread blocks that share a tile's keys
-  float* part;   // splits > 1: partial results [stream][kv head][tile][split][128][d], then (m, l) pairs
+  float* part;   // splits > 1: partial results [stream][kv head][tile][split][row][d], then (m, l) pairs
   float2* part_ml;
 };
 
@@ -110,11 +117,13 @@ __device__ __forceinline__ TileKeys tile_keys(const Geom& g, const StreamStep& s
   return t;
 }
 
-template <int D>
+template <int D, bool TWO>
 __global__ void __launch_bounds__(THREADS, 1)
     many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const Params pp) {
-  using L = Smem<D>;
+  using L = Smem<D, TWO>;
+  constexpr int NK = L::NK;
+  constexpr int ROWS = L::TILES * BM;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const FwdParams& p = pp.f;
@@ -126,8 +135,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tile = pp.q_tiles - 1 - blockIdx.x / pp.splits;
   const int h = blockIdx.y, s = blockIdx.z;
   const StreamStep st = stream_step(p, s);
-  const int row0 = tile * BM;
-  const int rows = min(BM, st.n * g.group - row0);
+  const int row0 = tile * ROWS;
+  const int rows = min(ROWS, st.n * g.group - row0);
   if (rows <= 0) return;
   const TileKeys tk = tile_keys(g, st, row0, rows);
   const int b0 = tk.first + (int)((long long)tk.count * split / pp.splits);
@@ -148,11 +157,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_full = bars;
   uint64_t* kv_full = bars + 1;      // K and V bytes of a stage have landed
-  uint64_t* qk_done = kv_full + NK;  // S_j in TMEM and K stage j % NK free
-  uint64_t* v8_empty = qk_done + NK; // V stage j % NK converted
+  uint64_t* k_empty = kv_full + NK;  // Q K^T with K of a stage is done
+  uint64_t* v8_empty = k_empty + NK; // V's bytes of a stage are converted
   uint64_t* v_full = v8_empty + NK;
   uint64_t* v_empty = v_full + NV;
-  uint64_t* p_full = v_empty + NV;
+  uint64_t* s_full = v_empty + NV;   // a group's next S is in TMEM
+  uint64_t* p_full = s_full + 2;     // ... and its P
   uint64_t* o_final = p_full + 2;
   uint64_t* sc_full = o_final + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -168,14 +178,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(q_full, 256);
     for (int i = 0; i < NK; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&qk_done[i], 1);
+      mbar_init(&k_empty[i], 1);
       mbar_init(&v8_empty[i], V_WARPS);
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(&v_full[i], V_WARPS);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
     mbar_init(o_final, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&sc_full[i], 1);
     *abort_flag = 0;
@@ -226,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float sc_next = scale_of(j + 1, pg_next);
       const int sg = j % NK;
       const uint32_t free_phase = ((j / NK) & 1) ^ 1;
-      ok = __all_sync(~0u, mbar_wait(&qk_done[sg], free_phase, wc) && mbar_wait(&v8_empty[sg], free_phase, wc));
+      ok = __all_sync(~0u, mbar_wait(&k_empty[sg], free_phase, wc) && mbar_wait(&v8_empty[sg], free_phase, wc));
       if (!ok || (p.ctl.debug_flags & VATTN_DEBUG_SKIP_ARRIVAL)) break;
       // one box of page_tokens rows for each page that holds a key to be read
       // (its first 16 keys may lie before the window: any of its groups of 16 names it)
@@ -301,38 +314,51 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t k_base = smem_u32(smem + L::OFF_K);
       const uint32_t v_base = smem_u32(smem + L::OFF_V);
       bool ok = mbar_wait(q_full, 0, wc);
-      auto issue_qk = [&](int j) -> bool {
+      // S of group w = Q (of its tile) K_j^T
+      auto issue_qk = [&](int j, int w, bool last_of_k) -> bool {
         const int sg = j % NK;
         if (!mbar_wait(&kv_full[sg], (j / NK) & 1, wc)) return false;
         tc_fence_after();
-        const uint32_t kb = k_base + sg * L::QK;
-        const uint32_t d_tmem = tmem + (uint32_t)((j & 1) * 128);
+        const uint32_t kb = k_base + sg * L::QK, qb = q_base + (TWO ? w : 0) * 2 * L::QK;
 #pragma unroll
         for (int part = 0; part < 2; ++part)  // hi, lo
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_ss_e4m3(d_tmem, desc_bytes<D>(q_base + part * L::QK + kk * 32), desc_bytes<D>(kb + kk * 32),
-                        idesc_e4m3_f32(BM, BN), part + kk > 0);
-        tc_commit(&qk_done[sg]);
+            mma_ss_e4m3(tmem + (uint32_t)(w * 128), desc_bytes<D>(qb + part * L::QK + kk * 32),
+                        desc_bytes<D>(kb + kk * 32), idesc_e4m3_f32(BM, BN), part + kk > 0);
+        tc_commit(&s_full[w]);
+        if (last_of_k) tc_commit(&k_empty[sg]);
         return true;
       };
-      if (ok) ok = issue_qk(0);
-      if (ok && nblk > 1) ok = issue_qk(1);
-      for (int j = 0; ok && j < nblk; ++j) {
-        const int w = j & 1;
-        if (!mbar_wait(&p_full[w], (j >> 1) & 1, wc)) break;
+      // O of group w += P V_j; i: the group's how-manieth block
+      auto issue_pv = [&](int j, int w, int i, bool last_of_v) -> bool {
         const int sg = j % NV;
-        if (!mbar_wait(&v_full[sg], (j / NV) & 1, wc)) break;
+        if (!mbar_wait(&p_full[w], i & 1, wc)) return false;
+        if (!mbar_wait(&v_full[sg], (j / NV) & 1, wc)) return false;
         tc_fence_after();
         const uint32_t vb = v_base + sg * L::V;
-        const uint32_t o_tmem = tmem + 256 + (uint32_t)(w * 128);
-        const uint32_t p_tmem = tmem + (uint32_t)(w * 128);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(o_tmem, p_tmem + kk * 8, smem_desc_sw128(vb + kk * 2048, 128 * 128, 1024), idesc_f16_pv(D),
-                 (j >= 2 || kk > 0) ? 1u : 0u);
-        tc_commit(&v_empty[sg]);
-        if (j + 2 < nblk) ok = issue_qk(j + 2);
+          mma_ts(tmem + 256 + (uint32_t)(w * 128), tmem + (uint32_t)(w * 128) + kk * 8,
+                 smem_desc_sw128(vb + kk * 2048, 128 * 128, 1024), idesc_f16_pv(D), (i > 0 || kk > 0) ? 1u : 0u);
+        if (last_of_v) tc_commit(&v_empty[sg]);
+        return true;
+      };
+      if constexpr (TWO) {
+        ok = ok && issue_qk(0, 0, false) && issue_qk(0, 1, true);
+        for (int j = 0; ok && j < nblk; ++j) {
+          ok = issue_pv(j, 0, j, false);
+          if (ok && j + 1 < nblk) ok = issue_qk(j + 1, 0, false);
+          ok = ok && issue_pv(j, 1, j, true);
+          if (ok && j + 1 < nblk) ok = issue_qk(j + 1, 1, true);
+        }
+      } else {
+        ok = ok && issue_qk(0, 0, true);
+        if (ok && nblk > 1) ok = issue_qk(1, 1, true);
+        for (int j = 0; ok && j < nblk; ++j) {
+          ok = issue_pv(j, j & 1, j >> 1, true);
+          if (ok && j + 2 < nblk) ok = issue_qk(j + 2, j & 1, true);
+        }
       }
       tc_commit(o_final);
       // every MMA this thread issued must be finished before TMEM is freed
@@ -341,22 +367,24 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // ---------------- softmax groups ----------------
     const int w = warp >> 2, quad = warp & 3;
-    const int row = quad * 32 + lane;
-    const bool real = row < rows;
-    const int tok = real ? (row0 + row) / g.group : 0;
-    const size_t out_row =
-        (size_t)(st.row0 + tok) * g.q_heads + h * g.group + (real ? row0 + row - tok * g.group : 0);
+    const int row = quad * 32 + lane;                    // in its tile
+    const int brow = (TWO ? w * BM : 0) + row;           // in the thread block's rows
+    const bool real = brow < rows;
+    const int tok = real ? (row0 + brow) / g.group : 0;
+    const int head = h * g.group + (real ? row0 + brow - tok * g.group : 0);
+    const size_t out_row = (size_t)(st.row0 + tok) * g.q_heads + head;
     int lo = 0, hi = 0;
     if (real) key_range(g, st, tok, &lo, &hi);
-    // half a query row a thread (the group's half): scaled, split into hi + lo, written in the MMA's layout
+    // the query row, scaled and split into hi + lo, in the MMA's layout.  One tile: the groups take half a row each.
     float c_row, poison;
     {
-      constexpr int NC = D / 32;  // 16-element chunks of half a row
+      constexpr int NC = TWO ? D / 16 : D / 32;  // 16-element chunks a thread
+      const int first = TWO ? 0 : w * NC;
+      uint8_t* q_hi = smem + L::OFF_Q + (TWO ? w : 0) * 2 * L::QK;
       uint4 x[2 * NC];
       uint32_t m = 0;
-      const uint4* src = (const uint4*)(p.q + (long long)(st.row0 + tok) * p.q_stride +
-                                        (long long)(h * g.group + (real ? row0 + row - tok * g.group : 0)) * D +
-                                        w * (D / 2));
+      const uint4* src =
+          (const uint4*)(p.q + (long long)(st.row0 + tok) * p.q_stride + (long long)head * D + first * 16);
 #pragma unroll
       for (int i = 0; i < 2 * NC; ++i) {
         x[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
@@ -364,10 +392,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
       }
       m = max(m & 0xffffu, m >> 16);
-      xch[w * 128 + row].x = __uint_as_float(m);
-      named_bar_sync(1, 256);
-      m = max(m, __float_as_uint(xch[(1 - w) * 128 + row].x));
-      named_bar_sync(1, 256);
+      if constexpr (!TWO) {
+        xch[w * 128 + row].x = __uint_as_float(m);
+        named_bar_sync(1, 256);
+        m = max(m, __float_as_uint(xch[(1 - w) * 128 + row].x));
+        named_bar_sync(1, 256);
+      }
       poison = m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
       const int sh = m == 0 ? 0 : min(7 - ((int)(m >> 7) - 127), 126);
       const float up = __int_as_float((sh + 127) << 23);
@@ -390,9 +420,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           hv[u] = hh[0] | (hh[1] << 16);
           lv[u] = ll[0] | (ll[1] << 16);
         }
-        const uint32_t at = byte_chunk<D>(row, w * NC + i);
-        *(uint4*)(smem + L::OFF_Q + at) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *(uint4*)(smem + L::OFF_Q + L::QK + at) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
+        const uint32_t at = byte_chunk<D>(row, first + i);
+        *(uint4*)(q_hi + at) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        *(uint4*)(q_hi + L::QK + at) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
       }
       fence_async_smem();
       mbar_arrive(q_full);
@@ -401,18 +431,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tS = tmem + lane_addr + (uint32_t)(w * 128);
     const uint32_t tO = tmem + lane_addr + 256u + (uint32_t)(w * 128);
     float m_ref = -INFINITY, l_sum = 0.f;
-    int qs = w;        // qk_done stage of this group's next block ...
-    uint32_t qph = 0;  // ... and its phase parity
     bool ok = true;
     for (int i = 0;; ++i) {
-      const int j = 2 * i + w;
+      const int j = TWO ? i : 2 * i + w;
       if (j >= nblk) break;
-      ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&qk_done[qs], qph, wc);
-      qs += 2;
-      if (qs >= NK) {
-        qs -= NK;
-        qph ^= 1u;
-      }
+      ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&s_full[w], i & 1, wc);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after();
@@ -502,32 +525,42 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (ok && !*abort_flag) ok = mbar_wait(o_final, 0, wc);
     ok = __all_sync(~0u, ok);
     tc_fence_after();
-    xch[w * 128 + row] = make_float2(m_ref, l_sum);
-    named_bar_sync(1, 256);
+    if constexpr (!TWO) {
+      xch[w * 128 + row] = make_float2(m_ref, l_sum);
+      named_bar_sync(1, 256);
+    }
     if (ok && !*abort_flag) {
-      const float2 other = xch[(1 - w) * 128 + row];
-      const float m = fmaxf(m_ref, other.x);
-      const float m0 = m == -INFINITY ? 0.f : m;
-      const float a_self = ex2(m_ref - m0), a_other = ex2(other.x - m0);
-      // a group without blocks has l = 0 and m = -inf
-      const float l = l_sum * a_self + other.y * a_other;
+      // TWO: the group's O is its tile's; else the two groups' halves of the keys are joined, half the channels each
+      float m = m_ref, l = l_sum, a0 = 1.f, a1 = 0.f;
+      bool both = false;
+      if constexpr (!TWO) {
+        const float2 other = xch[(1 - w) * 128 + row];
+        m = fmaxf(m_ref, other.x);
+        const float m0 = m == -INFINITY ? 0.f : m;
+        const float a_self = ex2(m_ref - m0), a_other = ex2(other.x - m0);
+        l = l_sum * a_self + other.y * a_other;  // a group without blocks has l = 0 and m = -inf
+        a0 = w == 0 ? a_self : a_other;
+        a1 = w == 0 ? a_other : a_self;
+        both = nblk >= 2;
+      }
       const bool whole = pp.splits == 1;
       const float norm = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      const float a0 = (w == 0 ? a_self : a_other) * norm;
-      const float a1 = (w == 0 ? a_other : a_self) * norm;
-      const bool have1 = nblk >= 2;
-      const uint32_t tO0 = tmem + lane_addr + 256u, tO1 = tmem + lane_addr + 384u;
-      const size_t pr = whole ? 0
-                              : ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + split) * BM + row;
+      a0 *= norm;
+      a1 *= norm;
+      const uint32_t t0 = TWO ? tO : tmem + lane_addr + 256u, t1 = tmem + lane_addr + 384u;
+      const size_t pr =
+          whole ? 0 : ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + split) * ROWS + brow;
+      constexpr int SPAN = TWO ? D : D / 2;
 #pragma unroll
-      for (int c0 = (w * D) / 2; c0 < ((w + 1) * D) / 2; c0 += 32) {
+      for (int c = 0; c < SPAN; c += 32) {
+        const int c0 = (TWO ? 0 : w * SPAN) + c;
         uint32_t x0[32], x1[32];
-        tmem_ld32(tO0 + c0, x0);
-        if (have1) tmem_ld32(tO1 + c0, x1);
+        tmem_ld32(t0 + c0, x0);
+        if (!TWO && both) tmem_ld32(t1 + c0, x1);
         tmem_wait_ld();
         float* o = reinterpret_cast<float*>(x0);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = o[c] * a0 + (have1 ? __uint_as_float(x1[c]) * a1 : 0.f);
+        for (int e = 0; e < 32; ++e) o[e] = o[e] * a0 + (!TWO && both ? __uint_as_float(x1[e]) * a1 : 0.f);
         if (real && whole) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * D + c0);
 #pragma unroll
@@ -541,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             dst[v4] = make_float4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
         }
       }
-      if (w == 0 && real) {
+      if ((TWO || w == 0) && real) {
         if (!whole)
           pp.part_ml[pr] = make_float2(m, l);
         else if (p.lse)
@@ -560,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Joins the splits of each row, in their order; one warp a row.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const Params pp) {
+__global__ void __launch_bounds__(256) join_kernel(const Params pp, int tile_rows) {
   const FwdParams& p = pp.f;
   const Geom& g = p.g;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -568,15 +601,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Params pp) {
   const StreamStep st = stream_step(p, s);
   const int all = st.n * g.group;
   if (r >= all) return;
-  const int tile = r / BM, row = r % BM;
-  const TileKeys tk = tile_keys(g, st, tile * BM, min(BM, all - tile * BM));
+  const int tile = r / tile_rows, row = r % tile_rows;
+  const TileKeys tk = tile_keys(g, st, tile * tile_rows, min(tile_rows, all - tile * tile_rows));
   if (tk.count == 0) return;
   constexpr int PER = D / 32;
   float acc[PER] = {};
   float m = -INFINITY, l = 0.f;
   for (int i = 0; i < pp.splits; ++i) {
     if ((long long)tk.count * i / pp.splits == (long long)tk.count * (i + 1) / pp.splits) continue;
-    const size_t pr = ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + i) * BM + row;
+    const size_t pr = ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + i) * tile_rows + row;
     const float2 ml = pp.part_ml[pr];
     const float m_new = fmaxf(m, ml.x), ref = m_new == -INFINITY ? 0.f : m_new;
     const float a = ex2(m - ref), e = ex2(ml.x - ref);
@@ -594,19 +627,34 @@ __global__ void __launch_bounds__(256) join_kernel(const Params pp) {
   if (lane == 0 && p.lse) p.lse[at] = (m - P_SHIFT + __log2f(l)) * 0.69314718055994531f;
 }
 
-int tiles_of(const Geom& g, long long max_new) { return (int)((max_new * g.group + BM - 1) / BM); }
+// Query rows a thread block takes (see TWO).
+int rows_of(const Geom& g, long long max_new) { return max_new * g.group > BM ? 2 * BM : BM; }
+int tiles_of(const Geom& g, long long max_new) {
+  const int rows = rows_of(g, max_new);
+  return (int)((max_new * g.group + rows - 1) / rows);
+}
 
-// Thread blocks per tile of rows: enough to use the 148 SMs when there are few tiles.
+// Thread blocks that share a tile's keys: what makes the waves of 148 thread
+// blocks fullest, each split costing 2% of a tile for its start and the join.
 int splits_of(const Geom& g, long long max_new) {
   const long long items = (long long)g.streams * g.kv_heads * tiles_of(g, max_new);
-  return items >= 148 ? 1 : (int)std::min<long long>(148 / items, 32);
+  int best = 1;
+  double least = 1e30;
+  for (int sp = 1; sp <= 32 && items * sp <= 148 * 8; ++sp) {
+    const double cost = (double)((items * sp + 147) / 148) / sp * (1 + 0.02 * (sp - 1));
+    if (cost < least) {
+      least = cost;
+      best = sp;
+    }
+  }
+  return best;
 }
 size_t part_rows(const Geom& g, long long max_new) {
   const int sp = splits_of(g, max_new);
-  return sp == 1 ? 0 : (size_t)g.streams * g.kv_heads * tiles_of(g, max_new) * sp * BM;
+  return sp == 1 ? 0 : (size_t)g.streams * g.kv_heads * tiles_of(g, max_new) * sp * rows_of(g, max_new);
 }
 
-template <int D>
+template <int D, bool TWO>
 cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   Params p;
   p.f = f;
@@ -620,15 +668,15 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   if (!make_tmap_pages(&tk, f.kc, D, f.g.page_tokens, heads, &err) ||
       !make_tmap_pages(&tv, f.vc, D, f.g.page_tokens, heads, &err))
     return cudaErrorInvalidValue;
-  auto kernel = many_kernel<D>;
-  constexpr int smem = Smem<D>::ALLOC;
+  auto kernel = many_kernel<D, TWO>;
+  constexpr int smem = Smem<D, TWO>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<dim3(p.q_tiles * p.splits, f.g.kv_heads, f.g.streams), THREADS, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   const int rows = (int)(f.max_new * f.g.group);
-  join_kernel<D><<<dim3((rows + 7) / 8, f.g.kv_heads, f.g.streams), 256, 0, stream>>>(p);
+  join_kernel<D><<<dim3((rows + 7) / 8, f.g.kv_heads, f.g.streams), 256, 0, stream>>>(p, rows_of(f.g, f.max_new));
   return cudaGetLastError();
 }
 
@@ -639,7 +687,10 @@ size_t cache_many_workspace(const cache::Geom& g, long long max_new) {
   return cache::many::part_rows(g, max_new) * (g.d + 2) * sizeof(float);
 }
 cudaError_t launch_cache_many(const cache::FwdParams& p, void* ws, cudaStream_t st) {
-  return p.g.d == 128 ? cache::many::launch<128>(p, ws, st) : cache::many::launch<64>(p, ws, st);
+  using namespace cache::many;
+  const bool two = rows_of(p.g, p.max_new) > BM;
+  if (p.g.d == 128) return two ? launch<128, true>(p, ws, st) : launch<128, false>(p, ws, st);
+  return two ? launch<64, true>(p, ws, st) : launch<64, false>(p, ws, st);
 }
 
 }  // namespace vattn
