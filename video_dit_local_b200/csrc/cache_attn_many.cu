@@ -52,6 +52,11 @@ constexpr float RESCALE = 8.0f;
 constexpr float P_SHIFT = 7.0f;
 constexpr int SUBS = BN / SCALE_TOKENS;
 
+// Of each 16 keys of a block: K's scale, log2 of V's, and 2^-log2 of V's.
+struct Scales {
+  float k[SUBS], e[SUBS], inv[SUBS];
+};
+
 template <int D, bool TWO>
 struct Smem {
   static constexpr int TILES = TWO ? 2 : 1;     // tiles of query rows
@@ -62,8 +67,8 @@ struct Smem {
   static constexpr int OFF_K = TILES * 2 * QK;
   static constexpr int OFF_V8 = OFF_K + NK * QK;  // V as cached, in step with K
   static constexpr int OFF_V = OFF_V8 + NK * QK;
-  static constexpr int OFF_SC = OFF_V + NV * V;              // NS x (8 K, 8 V) scales
-  static constexpr int OFF_XCH = OFF_SC + NS * 2 * SUBS * 4;
+  static constexpr int OFF_SC = OFF_V + NV * V;              // NS x Scales
+  static constexpr int OFF_XCH = OFF_SC + NS * (int)sizeof(Scales);
   static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
   static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 1 + NS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   float2* xch = reinterpret_cast<float2*>(smem + L::OFF_XCH);
-  float* scales = reinterpret_cast<float*>(smem + L::OFF_SC);
+  Scales* scales = reinterpret_cast<Scales*>(smem + L::OFF_SC);
   WaitCtx wc;
   wc.abort_flag = abort_flag;
   wc.timeout_ns = p.ctl.timeout_ns;
@@ -255,7 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         tma_load_3d(smem + L::OFF_V8 + at, &tm_v, &kv_full[sg], 0, 0, page * g.kv_heads + h);
       }
       ++issued;
-      if (lane < 16) scales[(j % NS) * 2 * SUBS + lane] = sc;
+      // 16 keys that are not read have scale 0: exponent -127, and P = 0
+      if (lane < 8) {
+        scales[j % NS].k[lane] = sc;
+      } else if (lane < 16) {
+        const int bits = __float_as_int(sc) & 0x7f800000;
+        scales[j % NS].e[lane - 8] = (float)((bits >> 23) - 127);
+        scales[j % NS].inv[lane - 8] = __int_as_float((254 << 23) - max(bits, 1 << 23));
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc_full[j % NS]);
       pg = pg_next;
@@ -442,13 +454,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t sr[4][32];
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(tS + q4 * 32, sr[q4]);
-      const float* sc = scales + (j % NS) * 2 * SUBS;
-      float f[SUBS], e[SUBS];  // x = S f + e
-#pragma unroll
-      for (int b = 0; b < SUBS; ++b) {
-        f[b] = fmaxf(c_row * sc[b], 1.17549435e-38f);  // > 0: a masked score stays -inf
-        e[b] = (float)((__float_as_int(sc[SUBS + b]) >> 23) - 127) + poison;
-      }
+      // x = S f + e for each 16 keys; f > 0, so that a masked score stays -inf
+      const Scales& sc = scales[j % NS];
+      auto factor = [&](int b) { return fmaxf(c_row * sc.k[b], 1.17549435e-38f); };
+      auto offset = [&](int b) { return sc.e[b] + poison; };
       tmem_wait_ld();
       const int from = lo - (b0 + j) * BN, to = hi - (b0 + j) * BN;
       if (from > 0 || to < BN) {
@@ -468,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           m0 = fmax3(m0, __uint_as_float(v[0]), __uint_as_float(v[1]));
           m1 = fmax3(m1, __uint_as_float(v[2]), __uint_as_float(v[3]));
         }
-        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), f[b], e[b]));
+        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(b), offset(b)));
       }
       bool need = false;
       float alpha = 1.f;
@@ -487,7 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int b2 = 0; b2 < 2; ++b2) {
           const int b = q4 * 2 + b2;
-          const float2 ff = make_float2(f[b], f[b]), ee = make_float2(e[b] - ref, e[b] - ref);
+          const float f = factor(b), e = offset(b) - ref;
+          const float2 ff = make_float2(f, f), ee = make_float2(e, e);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -497,9 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             sum = fadd2(sum, pr);
             pk[b2 * 8 + c] = pack_f16(pr.x, pr.y);
           }
-          // P 2^-log2(vs); an unused block's scale reads 0, exponent -127, with P = 0
-          const float inv = __int_as_float((254 << 23) - max(__float_as_int(sc[SUBS + b]) & 0x7f800000, 1 << 23));
-          l_sum = fmaf(sum.x + sum.y, inv, l_sum);
+          l_sum = fmaf(sum.x + sum.y, sc.inv[b], l_sum);
         }
         tmem_st16(tS + q4 * 16, pk);
       }
