@@ -8,21 +8,23 @@
 //    three thread blocks of four warps keep about 100 KB in flight on an SM,
 //    twice what the memory latency needs at full rate;
 //  - a fixed grid shares all streams' 128-key tiles evenly, whatever their
-//    lengths: thread block c of C takes tiles [c T / C, (c + 1) T / C) of the T
-//    tiles laid out stream by stream and head by head.  A (stream, head) that
+//    lengths: every thread block takes an equal run of the tiles, which are laid out stream by stream and head by head.  A (stream, head) that
 //    spans several thread blocks leaves partial results that a second kernel
 //    joins in a fixed order; it is launched early (programmatic dependent
 //    launch) so that only its joins are exposed.
 //  - the products run on mma.sync m16n8k16: 16 rows are far too few for a
-//    tcgen05 tile, the operands come from registers as they are converted, and
-//    the tensor pipe idles most of the time anyway.
+//    tcgen05 tile, and the operands come from registers as they are converted.
+//    Both are transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and
+//    channels fill the 16 rows of an instruction and the query rows its 8
+//    columns: half the instructions and accumulators of the other way round.
 //
 // Numbers: e4m3 bytes become f16 exactly.  A query row is scaled by a power of
 // two into f16's upper range, so its 8 significant bits are exact down to
-// 2^-29 of the row's largest element.  P is kept in (0, 2^14] as f16, 11
-// significant bits down to 2^-28 of the row's largest weight.  A V scale is a
-// power of two: it enters the exponent of P, x_j = s_j + log2(vs), and the row
-// sum takes P 2^-log2(vs), so that O needs no scale and no weight overflows.
+// 2^-29 of the row's largest element.  The reference m of a row moves when a
+// score passes it by more than 2^8; P = 2^(x - m + 7) <= 2^15 is f16, 11
+// significant bits down to 2^-21 of 2^m.  A V scale is a power of two: it
+// enters the exponent of P, x_j = s_j + log2(vs), and the row sum takes
+// P 2^-log2(vs), so that O needs no scale and no weight overflows.
 #include "cache.cuh"
 
 namespace vattn {
@@ -36,7 +38,8 @@ constexpr int TILE = WARPS * STEP;   // keys of a thread block's step
 constexpr int ROWS = 16;
 constexpr int CTAS_PER_SM = 3;
 constexpr int GRID = 148 * CTAS_PER_SM;
-constexpr float P_SHIFT = 14.0f;     // P = 2^(x - m + 14)
+constexpr float P_SHIFT = 7.0f;      // P = 2^(x - m + 7)
+constexpr float RESCALE = 8.0f;
 
 // Two partial results a thread block: of the (stream, head) that began before
 // its tiles (slot 0) and of the one that goes on after them (slot 1).
@@ -100,42 +103,62 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+// 8 x 8 f16 matrix, a row's pair of columns per lane -> its transpose.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // Shared-memory layouts of a step.  Lane (g, t) = (lane / 4, lane % 4) of the
 // MMA fragments reads, eight lanes (two g, four t) at a time:
-//  K: 16 bytes at chunk t (+ 4) of row ... + (g & 1): at d = 128 odd rows keep
-//     their chunks 4 further on, so that the eight lanes meet all 32 banks
-//     (at d = 64 two rows fill them anyway);
-//  V: chunk g of rows 4 t + r: chunks are turned by 2 (row / 4).  d = 64: 8-byte
-//     reads by 16 lanes; rows 4..7 and 12..15 swap with their neighbours and
-//     rows 8..15 turn by two chunks.
+//  K: 16 bytes at chunk t (+ 4) of row g (+ 8): at d = 128 odd rows keep their
+//     chunks 4 further on, so that the eight lanes meet all 32 banks (at d = 64
+//     two rows fill them anyway);
+//  V: chunk g of rows 2 t + const: chunks are turned by 2 (row / 2).  d = 64:
+//     8-byte reads by 16 lanes; rows with bit 1 set swap with their neighbours,
+//     rows with bit 2 set turn by two chunks.
 template <int D>
 __device__ __forceinline__ uint32_t k_at(int row, int chunk) {
   return D == 128 ? row * 128 + ((chunk ^ ((row & 1) << 2)) << 4) : row * 64 + (chunk << 4);
 }
 template <int D>
 __device__ __forceinline__ uint32_t v_at(int row, int chunk) {
-  return D == 128 ? row * 128 + ((chunk ^ (((row >> 2) & 3) << 1)) << 4)
-                  : (row ^ ((row >> 2) & 1)) * 64 + ((chunk ^ (((row >> 3) & 1) << 1)) << 4);
+  return D == 128 ? row * 128 + ((chunk ^ (((row >> 1) & 3) << 1)) << 4)
+                  : (row ^ ((row >> 1) & 1)) * 64 + ((chunk ^ (((row >> 2) & 1) << 1)) << 4);
 }
 
-// Thread blocks that share `total` tiles, each with one at least: block c
-// takes tiles [c total / sharers, (c + 1) total / sharers).
-__device__ __forceinline__ int sharers(long long total) { return (int)min((long long)GRID, total); }
+// `total` tiles shared evenly: each of the first `extra` thread blocks takes
+// per + 1 of them, each of the others `per` (blocks past total take none).
+struct Shares {
+  long long per, extra;
+  __device__ __forceinline__ explicit Shares(long long total) {
+    per = total < (1ll << 31) ? (uint32_t)total / GRID : total / GRID;
+    extra = total - per * GRID;
+  }
+  __device__ __forceinline__ long long first(int block) const { return block * per + min((long long)block, extra); }
+  __device__ __forceinline__ int owner(long long tile) const {
+    const long long wide = extra * (per + 1);  // tiles of the blocks that take one more
+    if (tile < wide) return per < (1ll << 30) && wide < (1ll << 31) ? (uint32_t)tile / (uint32_t)(per + 1) : tile / (per + 1);
+    const long long r = tile - wide;
+    return (int)extra + (r < (1ll << 31) && per < (1ll << 31) ? (uint32_t)r / (uint32_t)per : r / per);
+  }
+};
 
 // The tiles of one stream, for each kv head: keys [base, end), `tiles` of TILE.
 struct StreamTiles {
   StreamStep st;
-  int base, end, tiles;
+  int lo, base, end, tiles;  // base: lo rounded down to a step
 };
 __device__ __forceinline__ StreamTiles stream_tiles(const FwdParams& p, int s) {
   StreamTiles r;
   r.st = stream_step(p, s);
-  r.base = r.end = r.tiles = 0;
+  r.lo = r.base = r.end = r.tiles = 0;
   if (r.st.n > 0) {
-    int lo, hi, x;
-    key_range(p.g, r.st, 0, &lo, &x);
+    int hi, x;
+    key_range(p.g, r.st, 0, &r.lo, &x);
     key_range(p.g, r.st, r.st.n - 1, &x, &hi);
-    r.base = lo & ~(STEP - 1);
+    r.base = r.lo & ~(STEP - 1);
     r.end = max(hi, r.base);
     r.tiles = max(1, (r.end - r.base + TILE - 1) / TILE);  // one that is empty still writes its rows
   }
@@ -185,10 +208,11 @@ __device__ __forceinline__ Place find_stream(const FwdParams& p, Wanted wanted, 
   return r;
 }
 
-// UP: rows 8..15 exist.
-template <int D, bool UP>
+// NT: blocks of 8 query rows.
+template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdParams p, void* ws) {
   using R = Ring<D>;
+  constexpr int KS = D / 16;  // k-steps of S^T; m-tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long sums[WARPS];
   __shared__ Place place;
@@ -200,12 +224,16 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
   const uint32_t ring = smem_u32(mine);
 
   const Place pl = find_stream<THREADS>(
-      p, [](long long total) { return blockIdx.x < sharers(total) ? blockIdx.x * total / sharers(total) : -1; }, sums,
-      &place);
-  const int share = sharers(pl.total);
-  if ((int)blockIdx.x >= share) return;
-  long long at = blockIdx.x * pl.total / share;
-  const long long stop = (blockIdx.x + 1) * pl.total / share;
+      p,
+      [](long long total) {
+        const long long t = Shares(total).first(blockIdx.x);
+        return t < total ? t : -1;
+      },
+      sums, &place);
+  const Shares shares(pl.total);
+  long long at = shares.first(blockIdx.x);
+  const long long stop = shares.first(blockIdx.x + 1);
+  if (at >= stop) return;
   int s = pl.stream;
   long long first = pl.first;  // first tile of stream s
   StreamTiles sp = stream_tiles(p, s);
@@ -215,55 +243,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       first += (long long)sp.tiles * g.kv_heads;
       sp = stream_tiles(p, ++s);
     }
-    const int h = (int)((at - first) / sp.tiles);
-    const int k0 = (int)((at - first) % sp.tiles);
+    const long long in_stream = at - first;
+    const int h = in_stream < (1ll << 31) ? (uint32_t)in_stream / (uint32_t)sp.tiles : (int)(in_stream / sp.tiles);
+    const int k0 = (int)(in_stream - (long long)h * sp.tiles);
     const int k1 = (int)min((long long)sp.tiles, k0 + (stop - at));
     at += k1 - k0;
     const int rows = sp.st.n * g.group;
-
-    // query rows fg and fg + 8 as f16 MMA fragments, each row scaled by a power of two
-    uint32_t qf[D / 16][4];
-    float c_row[2], poison[2];
-    int lo[2], hi[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = fg + 8 * u;
-      const bool in = r < rows && (u == 0 || UP);
-      const int tok = in ? r / g.group : 0;
-      const __nv_bfloat16* src = p.q + (long long)(sp.st.row0 + tok) * p.q_stride +
-                                 (long long)(h * g.group + (in ? r - tok * g.group : 0)) * D;
-      uint2 w[D / 16];
-      uint32_t m = 0;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        w[kk] = in ? __ldg((const uint2*)(src + (kk >> 2) * 64 + 16 * ft + 4 * (kk & 3))) : make_uint2(0, 0);
-        m = __vmaxu2(m, __vmaxu2(w[kk].x & 0x7fff7fffu, w[kk].y & 0x7fff7fffu));
-      }
-      m = max(m & 0xffffu, m >> 16);
-      m = max(m, __shfl_xor_sync(~0u, m, 1));
-      m = max(m, __shfl_xor_sync(~0u, m, 2));
-      poison[u] = m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
-      const int sh = m == 0 ? 0 : min(14 - ((int)(m >> 7) - 127), 126);
-      const float up = __int_as_float((sh + 127) << 23);
-      c_row[u] = p.scale_log2 * __int_as_float((127 - sh) << 23);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        qf[kk][u] = pack_f16(bf16lo(w[kk].x) * up, bf16hi(w[kk].x) * up);
-        qf[kk][u + 2] = pack_f16(bf16lo(w[kk].y) * up, bf16hi(w[kk].y) * up);
-      }
-      key_range(g, sp.st, tok, &lo[u], &hi[u]);
-    }
-    int all_lo, all_hi, x;  // keys that every row sees
-    key_range(g, sp.st, 0, &x, &all_hi);
-    key_range(g, sp.st, sp.st.n - 1, &all_lo, &x);
-    int min_lo, max_hi;
-    key_range(g, sp.st, 0, &min_lo, &x);
-    key_range(g, sp.st, sp.st.n - 1, &x, &max_hi);
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    const int min_lo = sp.lo, max_hi = sp.end;
 
     // steps of this warp: keys sp.base + (k * WARPS + warp) * STEP, k in [k0, k1)
     const int* table = p.table + (long long)s * g.width;
@@ -289,21 +275,21 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       if (k < k1) {
         const int key0 = step_key(k);
         const uint32_t dst = ring + ((k - k0) % R::STAGES) * R::STAGE;
-        const int in_page = key0 & (g.page_tokens - 1);
-        const long long row0 = cache_row(g, max(pg0, 0), h, in_page);
-        // the second half lies in the same page unless pages hold 16 tokens
+        const long long row0 = cache_row(g, max(pg0, 0), h, key0 & (g.page_tokens - 1));
         const long long row1 = cache_row(g, max(pg1, 0), h, (key0 + SCALE_TOKENS) & (g.page_tokens - 1));
         constexpr int CH = D / 16, RP = 32 / CH;
         const int c = lane % CH;
+        const bool whole = pg0 >= 0 && pg1 >= 0 && key0 >= min_lo && key0 + STEP <= max_hi;
+        const long long off0 = row0 * D + (lane / CH) * D + c * 16, off1 = row1 * D + (lane / CH) * D + c * 16;
 #pragma unroll
         for (int i = 0; i < STEP / RP; ++i) {
           const int r = i * RP + lane / CH;
           const bool second = i * RP >= SCALE_TOKENS;
-          const int key = key0 + r;
-          const bool in = (second ? pg1 : pg0) >= 0 && key < max_hi && key >= min_lo;
-          const long long off = ((second ? row1 - SCALE_TOKENS : row0) + r) * D + c * 16;
-          cp16(dst + k_at<D>(r, c), p.kc + (in ? off : 0), in);
-          cp16(dst + R::HALF + v_at<D>(r, c), p.vc + (in ? off : 0), in);
+          bool in = true;
+          if (!whole) in = (second ? pg1 : pg0) >= 0 && key0 + r < max_hi && key0 + r >= min_lo;
+          const long long off = in ? (second ? off1 : off0) + (i * RP % SCALE_TOKENS) * D : 0;
+          cp16(dst + k_at<D>(r, c), p.kc + off, in);
+          cp16(dst + R::HALF + v_at<D>(r, c), p.vc + off, in);
         }
         if (lane < 4) {
           const bool in = (lane & 1 ? pg1 : pg0) >= 0;
@@ -313,13 +299,66 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       }
       cp_commit();
     };
-    __syncwarp();
     fetch_pages(k0);
 #pragma unroll
     for (int i = 0; i < R::STAGES - 1; ++i) {
       load(k0 + i);
       fetch_pages(k0 + i + 1);
     }
+
+    // query rows fg (+ 8) as f16 MMA fragments, each row scaled by a power of two; then what belongs to
+    // the rows 2 ft, 2 ft + 1 (+ 8) whose scores this lane holds
+    uint32_t qf[NT][KS][2];
+    float c_row[NT][2], poison[NT][2];
+    int lo[NT][2], hi[NT][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int r = fg + 8 * u;
+      const bool in = r < rows;
+      const int tok = in ? r / g.group : 0;
+      const __nv_bfloat16* src = p.q + (long long)(sp.st.row0 + tok) * p.q_stride +
+                                 (long long)(h * g.group + (in ? r - tok * g.group : 0)) * D;
+      uint2 w[KS];
+      uint32_t m = 0;
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        w[kk] = in ? __ldg((const uint2*)(src + (kk >> 2) * 64 + 16 * ft + 4 * (kk & 3))) : make_uint2(0, 0);
+        m = __vmaxu2(m, __vmaxu2(w[kk].x & 0x7fff7fffu, w[kk].y & 0x7fff7fffu));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, __shfl_xor_sync(~0u, m, 1));
+      m = max(m, __shfl_xor_sync(~0u, m, 2));
+      const float bad = m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
+      const int sh = m == 0 ? 0 : min(14 - ((int)(m >> 7) - 127), 126);
+      const float up = __int_as_float((sh + 127) << 23);
+      const float down = p.scale_log2 * __int_as_float((127 - sh) << 23);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        qf[u][kk][0] = pack_f16(bf16lo(w[kk].x) * up, bf16hi(w[kk].x) * up);
+        qf[u][kk][1] = pack_f16(bf16lo(w[kk].y) * up, bf16hi(w[kk].y) * up);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c_row[u][e] = __shfl_sync(~0u, down, (2 * ft + e) * 4);
+        poison[u][e] = __shfl_sync(~0u, bad, (2 * ft + e) * 4);
+        const int row = 2 * ft + e + 8 * u;
+        key_range(g, sp.st, row < rows ? row / g.group : 0, &lo[u][e], &hi[u][e]);
+      }
+    }
+    int all_lo, all_hi, x;  // keys that every row sees
+    key_range(g, sp.st, 0, &x, &all_hi);
+    key_range(g, sp.st, sp.st.n - 1, &all_lo, &x);
+
+    float o[NT][KS][4];
+    float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+#pragma unroll
+      for (int j = 0; j < KS; ++j) o[u][j][0] = o[u][j][1] = o[u][j][2] = o[u][j][3] = 0.f;
+      m_run[u][0] = m_run[u][1] = -INFINITY;
+      l_run[u][0] = l_run[u][1] = 0.f;
+    }
+
     for (int k = k0; k < k1; ++k) {
       load(k + R::STAGES - 1);
       fetch_pages(k + R::STAGES);
@@ -328,91 +367,104 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       const uint32_t st = ring + ((k - k0) % R::STAGES) * R::STAGE;
       const int key0 = step_key(k);
       if (key0 < max_hi) {
-        // S = Q K^T, 16 rows x 32 keys: column n of tile j is key
-        // 16 (j / 2) + 4 (n / 2) + 2 (j % 2) + n % 2, so that a thread's columns are the four keys
-        // whose V rows it reads
-        float sc[4][4];
+        // S^T: 16-key tile b, rows fg and fg + 8
+        float sc[NT][2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-          const int r = 16 * (j >> 1) + 4 * (fg >> 1) + 2 * (j & 1) + (fg & 1);
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u) sc[u][b][0] = sc[u][b][1] = sc[u][b][2] = sc[u][b][3] = 0.f;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
-            const uint4 w = lds128(st + k_at<D>(r, ft + 4 * c));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            const uint4 w0 = lds128(st + k_at<D>(16 * b + fg, ft + 4 * c));
+            const uint4 w1 = lds128(st + k_at<D>(16 * b + fg + 8, ft + 4 * c));
+            const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, e[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma16816(sc[j], qf[c * 4 + e], e4m3x2_to_f16x2((uint16_t)(ww[e] & 0xffffu)),
-                       e4m3x2_to_f16x2((uint16_t)(ww[e] >> 16)));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t f[4] = {
+                  e4m3x2_to_f16x2((uint16_t)(a[i] & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(e[i] & 0xffffu)),
+                  e4m3x2_to_f16x2((uint16_t)(a[i] >> 16)), e4m3x2_to_f16x2((uint16_t)(e[i] >> 16))};
+#pragma unroll
+              for (int u = 0; u < NT; ++u) mma16816(sc[u][b], f, qf[u][c * 4 + i][0], qf[u][c * 4 + i][1]);
+            }
           }
         }
+        const bool whole = key0 >= all_lo && key0 + STEP <= all_hi;
         float kf[2], ev[2], inv[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           kf[b] = lds32(st + 2 * R::HALF + b * 4);
-          const int e = (__float_as_int(lds32(st + 2 * R::HALF + 8 + b * 4)) >> 23) - 127;
-          ev[b] = (float)e;
-          inv[b] = __int_as_float((127 - max(e, -126)) << 23);
+          const int bits = __float_as_int(lds32(st + 2 * R::HALF + 8 + b * 4)) & 0x7f800000;
+          ev[b] = (float)((bits >> 23) - 127);
+          inv[b] = __int_as_float((254 << 23) - max(bits, 1 << 23));
         }
-        const bool whole = key0 >= all_lo && key0 + STEP <= all_hi;
-        uint32_t pf[2][4];  // P as MMA fragments, 16 keys each
-        bool moved = false;
-        float alpha[2] = {1.f, 1.f};
+        uint32_t pf[NT][2][2];  // P^T as MMA fragments
+        bool over = false;
+        float mx[NT][2];
 #pragma unroll
-        for (int u = 0; u < (UP ? 2 : 1); ++u) {
-          float mx = -INFINITY;
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float f = fmaxf(c_row[u] * kf[j >> 1], 1.17549435e-38f), e = ev[j >> 1] + poison[u];
+          for (int e = 0; e < 2; ++e) {
+            mx[u][e] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float v = fmaf(sc[j][2 * u + i], f, e);
-              if (!whole) {
-                const int key = key0 + 16 * (j >> 1) + 4 * ft + 2 * (j & 1) + i;
-                if (key < lo[u] || key >= hi[u]) v = -INFINITY;
+            for (int b = 0; b < 2; ++b) {
+              const float f = fmaxf(c_row[u][e] * kf[b], 1.17549435e-38f), off = ev[b] + poison[u][e];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v = fmaf(sc[u][b][2 * i + e], f, off);
+                if (!whole) {
+                  const int key = key0 + 16 * b + fg + 8 * i;
+                  if (key < lo[u][e] || key >= hi[u][e]) v = -INFINITY;
+                }
+                sc[u][b][2 * i + e] = v;
+                mx[u][e] = fmaxf(mx[u][e], v);
               }
-              sc[j][2 * u + i] = v;
-              mx = fmaxf(mx, v);
             }
+            over = over || mx[u][e] > m_run[u][e] + RESCALE;
           }
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-          if (mx > m_run[u]) {
-            alpha[u] = ex2(m_run[u] - mx);
-            m_run[u] = mx;
-            moved = true;
-          }
-          const float ref = (m_run[u] == -INFINITY ? 0.f : m_run[u]) - P_SHIFT;
-          float sum[2] = {0.f, 0.f};
+        if (__any_sync(~0u, over)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float a = ex2(sc[j][2 * u] - ref), b = ex2(sc[j][2 * u + 1] - ref);
-            sum[j >> 1] += a + b;
-            pf[j >> 1][(j & 1) * 2 + u] = pack_f16(a, b);
-          }
-          l_run[u] = l_run[u] * alpha[u] + (sum[0] * inv[0] + sum[1] * inv[1]);
-        }
-        if (!UP) {
-          pf[0][1] = pf[0][3] = pf[1][1] = pf[1][3] = 0;
-        }
-        if (__any_sync(~0u, moved)) {
+          for (int u = 0; u < NT; ++u) {
+            float alpha[2];
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][0] *= alpha[0];
-            o[j][1] *= alpha[0];
-            if (UP) {
-              o[j][2] *= alpha[1];
-              o[j][3] *= alpha[1];
+            for (int e = 0; e < 2; ++e) {
+              float m = mx[u][e];
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
+              const float m_new = fmaxf(m_run[u][e], m);
+              alpha[e] = m_new == -INFINITY ? 1.f : ex2(m_run[u][e] - m_new);
+              m_run[u][e] = m_new;
+              l_run[u][e] *= alpha[e];
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              o[u][j][0] *= alpha[0];
+              o[u][j][1] *= alpha[1];
+              o[u][j][2] *= alpha[0];
+              o[u][j][3] *= alpha[1];
             }
           }
         }
-        // O += P V: column n = fg of channel tile j is channel (D / 8) fg + j
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int u = 0; u < NT; ++u) {
+          const float ref0 = (m_run[u][0] == -INFINITY ? 0.f : m_run[u][0]) - P_SHIFT;
+          const float ref1 = (m_run[u][1] == -INFINITY ? 0.f : m_run[u][1]) - P_SHIFT;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float a0 = ex2(sc[u][b][0] - ref0), a1 = ex2(sc[u][b][1] - ref1);
+            const float b0 = ex2(sc[u][b][2] - ref0), b1 = ex2(sc[u][b][3] - ref1);
+            l_run[u][0] = fmaf(a0 + b0, inv[b], l_run[u][0]);
+            l_run[u][1] = fmaf(a1 + b1, inv[b], l_run[u][1]);
+            pf[u][b][0] = transpose8x8(pack_f16(a0, a1));
+            pf[u][b][1] = transpose8x8(pack_f16(b0, b1));
+          }
+        }
+        // O^T += V^T P^T: rows fg, fg + 8 of channel tile j are the channels (D / 8) fg + 2 j, + 1
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
           uint32_t w[4][D / 32];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int row = 16 * ks + 4 * ft + r;
+            const int row = 16 * b + 2 * ft + (r & 1) + 8 * (r >> 1);
             if constexpr (D == 128) {
               const uint4 v = lds128(st + R::HALF + v_at<D>(row, fg));
               w[r][0] = v.x;
@@ -430,10 +482,15 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
             // four keys' bytes of four channels -> key pairs of each channel
             const uint32_t a0 = __byte_perm(w[0][q4], w[1][q4], 0x5140), a1 = __byte_perm(w[0][q4], w[1][q4], 0x7362);
             const uint32_t b0 = __byte_perm(w[2][q4], w[3][q4], 0x5140), b1 = __byte_perm(w[2][q4], w[3][q4], 0x7362);
-            mma16816(o[q4 * 4], pf[ks], e4m3x2_to_f16x2((uint16_t)(a0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b0 & 0xffffu)));
-            mma16816(o[q4 * 4 + 1], pf[ks], e4m3x2_to_f16x2((uint16_t)(a0 >> 16)), e4m3x2_to_f16x2((uint16_t)(b0 >> 16)));
-            mma16816(o[q4 * 4 + 2], pf[ks], e4m3x2_to_f16x2((uint16_t)(a1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b1 & 0xffffu)));
-            mma16816(o[q4 * 4 + 3], pf[ks], e4m3x2_to_f16x2((uint16_t)(a1 >> 16)), e4m3x2_to_f16x2((uint16_t)(b1 >> 16)));
+            const uint32_t f0[4] = {e4m3x2_to_f16x2((uint16_t)(a0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(a0 >> 16)),
+                                    e4m3x2_to_f16x2((uint16_t)(b0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b0 >> 16))};
+            const uint32_t f1[4] = {e4m3x2_to_f16x2((uint16_t)(a1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(a1 >> 16)),
+                                    e4m3x2_to_f16x2((uint16_t)(b1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b1 >> 16))};
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+              mma16816(o[u][q4 * 2], f0, pf[u][b][0], pf[u][b][1]);
+              mma16816(o[u][q4 * 2 + 1], f1, pf[u][b][0], pf[u][b][1]);
+            }
           }
         }
       }
@@ -447,19 +504,19 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       float* mo = (float*)mine;
       float2* ml = (float2*)(mine + ROWS * D * 4);
 #pragma unroll
-      for (int u = 0; u < (UP ? 2 : 1); ++u) {
-        float l = l_run[u];
-        l += __shfl_xor_sync(~0u, l, 1);
-        l += __shfl_xor_sync(~0u, l, 2);
-        if (ft == 0) ml[fg + 8 * u] = make_float2(m_run[u], l);
-        // channels (D/8) fg' of column n = 2 ft, 2 ft + 1
+      for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int e = 0; e < 2; ++e) {
+          float l = l_run[u][e];
 #pragma unroll
-          for (int j = 0; j < D / 8; j += 4)
-            *(float4*)(mo + (fg + 8 * u) * D + (D / 8) * (2 * ft + i) + j) =
-                make_float4(o[j][2 * u + i], o[j + 1][2 * u + i], o[j + 2][2 * u + i], o[j + 3][2 * u + i]);
-      }
+          for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(~0u, l, w);
+          const int row = 2 * ft + e + 8 * u;
+          if (fg == 0) ml[row] = make_float2(m_run[u][e], l);
+#pragma unroll
+          for (int j = 0; j < KS; j += 2)
+            *(float4*)(mo + row * D + (D / 8) * fg + 2 * j) =
+                make_float4(o[u][j][e], o[u][j][2 + e], o[u][j + 1][e], o[u][j + 1][2 + e]);
+        }
     }
     __syncthreads();
     const bool complete = k0 == 0 && k1 == sp.tiles;
@@ -473,10 +530,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
         ml[w] = ((const float2*)(smem + w * R::PER_WARP + ROWS * D * 4))[r];
         m = fmaxf(m, ml[w].x);
       }
+      const float m0 = m == -INFINITY ? 0.f : m;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float a = ml[w].x == -INFINITY && ml[w].y == 0.f ? 0.f : ex2(ml[w].x - (m == -INFINITY ? 0.f : m));
+        const float a = ex2(ml[w].x - m0);
         const float4 v = *(const float4*)(smem + w * R::PER_WARP + (r * D + c) * 4);
         l += ml[w].y * a;
         acc.x += v.x * a;
@@ -532,8 +590,8 @@ __global__ void __launch_bounds__(128) join_kernel(const FwdParams p, void* ws) 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (sp.tiles == 0) return;
   const long long t0 = before + (long long)h * sp.tiles, t1 = t0 + sp.tiles - 1;
-  const int share = sharers(total);
-  const int c0 = (int)(((t0 + 1) * share - 1) / total), c1 = (int)(((t1 + 1) * share - 1) / total);
+  const Shares shares(total);
+  const int c0 = shares.owner(t0), c1 = shares.owner(t1);
   if (c0 == c1) return;
   const int rows = sp.st.n * g.group;
   for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
@@ -565,8 +623,7 @@ __global__ void __launch_bounds__(128) join_kernel(const FwdParams p, void* ws) 
 template <int D>
 cudaError_t launch(const FwdParams& p, void* ws, cudaStream_t st) {
   constexpr int smem = Ring<D>::TOTAL;
-  const bool up = p.max_new * p.g.group > 8;
-  auto kernel = up ? few_kernel<D, true> : few_kernel<D, false>;
+  auto kernel = p.max_new * p.g.group > 8 ? few_kernel<D, 2> : few_kernel<D, 1>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<GRID, THREADS, smem, st>>>(p, ws);
