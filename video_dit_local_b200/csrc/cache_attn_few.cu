@@ -558,66 +558,102 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
   }
 }
 
-// Joins the partial results of each (stream, head) that several thread blocks share.
+// Joins the partial results of each row that several thread blocks share: their
+// weights first, then groups of d / 4 threads take every so-manieth one, with
+// several loads in flight.
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const FwdParams p, void* ws) {
+  constexpr int LANES = D / 4, GROUPS = 128 / LANES;
   __shared__ long long part[8];
+  __shared__ float weight[GRID];
+  __shared__ float red[4];
+  __shared__ float4 accs[128];
   const Geom& g = p.g;
-  const int s = blockIdx.x / g.kv_heads, h = blockIdx.x % g.kv_heads;
-  // first tile of stream s = tiles of the streams before it
-  long long before = 0, total = 0;
-  {
-    const int t = threadIdx.x;
-    long long mine = 0, all = 0;
-    for (int i = t; i < g.streams; i += 128) {
-      const int n = stream_tiles(p, i).tiles;
-      all += n;
-      if (i < s) mine += n;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      mine += __shfl_xor_sync(~0u, mine, o);
-      all += __shfl_xor_sync(~0u, all, o);
-    }
-    if ((t & 31) == 0) {
-      part[t >> 5] = mine;
-      part[4 + (t >> 5)] = all;
-    }
-    __syncthreads();
-    before = (part[0] + part[1] + part[2] + part[3]) * g.kv_heads;
-    total = (part[4] + part[5] + part[6] + part[7]) * g.kv_heads;
+  const int t = threadIdx.x;
+  const int s = blockIdx.x / g.kv_heads, h = blockIdx.x % g.kv_heads, r = blockIdx.y;
+  // first tile of stream s, and all tiles
+  long long mine = 0, all = 0;
+  for (int i = t; i < g.streams; i += 128) {
+    const int n = stream_tiles(p, i).tiles;
+    all += n;
+    if (i < s) mine += n;
   }
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(~0u, mine, o);
+    all += __shfl_xor_sync(~0u, all, o);
+  }
+  if ((t & 31) == 0) {
+    part[t >> 5] = mine;
+    part[4 + (t >> 5)] = all;
+  }
+  __syncthreads();
+  const long long before = (part[0] + part[1] + part[2] + part[3]) * g.kv_heads;
+  const long long total = (part[4] + part[5] + part[6] + part[7]) * g.kv_heads;
   const StreamTiles sp = stream_tiles(p, s);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (sp.tiles == 0) return;
-  const long long t0 = before + (long long)h * sp.tiles, t1 = t0 + sp.tiles - 1;
+  if (r >= sp.st.n * g.group) return;
+  const long long t0 = before + (long long)h * sp.tiles;
   const Shares shares(total);
-  const int c0 = shares.owner(t0), c1 = shares.owner(t1);
+  const int c0 = shares.owner(t0), c1 = shares.owner(t0 + sp.tiles - 1);
   if (c0 == c1) return;
-  const int rows = sp.st.n * g.group;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = c0; b <= c1; ++b) {
-      const int slot = b * 2 + (b == c0 ? 1 : 0);
-      const float2 ml = __ldcg(slot_ml(ws, D, slot) + r);
-      const float4 v = __ldcg((const float4*)(slot_o(ws, D, slot) + r * D + c));
-      const float m_new = fmaxf(m, ml.x), ref = m_new == -INFINITY ? 0.f : m_new;
-      const float a = ex2(m - ref), e = ex2(ml.x - ref);
-      l = l * a + ml.y * e;
-      acc.x = acc.x * a + v.x * e;
-      acc.y = acc.y * a + v.y * e;
-      acc.z = acc.z * a + v.z * e;
-      acc.w = acc.w * a + v.w * e;
-      m = m_new;
+  const int n = c1 - c0 + 1;
+  // partial result i: block c0 keeps it in its second slot, the others in their first
+  auto slot_of = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
+  auto block_reduce = [&](float v, bool sum) {
+    for (int o = 16; o > 0; o >>= 1) {
+      const float w = __shfl_xor_sync(~0u, v, o);
+      v = sum ? v + w : fmaxf(v, w);
     }
-    const int tok = r / g.group;
-    const size_t at_o = (size_t)(sp.st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *(uint2*)(p.o + at_o * D + c) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (c == 0 && p.lse) p.lse[at_o] = (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
+    if ((t & 31) == 0) red[t >> 5] = v;
+    __syncthreads();
+    return sum ? (red[0] + red[1]) + (red[2] + red[3]) : fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  };
+  constexpr int PER = (GRID + 127) / 128;
+  float2 ml[PER];
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    ml[i] = t + 128 * i < n ? __ldcg(slot_ml(ws, D, slot_of(t + 128 * i)) + r) : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, ml[i].x);
   }
+  m = block_reduce(m, false);
+  const float m0 = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (t + 128 * i < n) {
+      const float w = ex2(ml[i].x - m0);
+      weight[t + 128 * i] = w;
+      l += ml[i].y * w;
+    }
+  l = block_reduce(l, true);
+  const int c = (t % LANES) * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = t / LANES; i < n; i += GROUPS) {
+    const float4 v = __ldcg((const float4*)(slot_o(ws, D, slot_of(i)) + r * D + c));
+    const float w = weight[i];
+    acc.x = fmaf(v.x, w, acc.x);
+    acc.y = fmaf(v.y, w, acc.y);
+    acc.z = fmaf(v.z, w, acc.z);
+    acc.w = fmaf(v.w, w, acc.w);
+  }
+  accs[t] = acc;
+  __syncthreads();
+  if (t >= LANES) return;
+  for (int i = 1; i < GROUPS; ++i) {
+    const float4 v = accs[t + i * LANES];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  const int tok = r / g.group;
+  const size_t at_o = (size_t)(sp.st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *(uint2*)(p.o + at_o * D + c) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (c == 0 && p.lse) p.lse[at_o] = (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D>
@@ -630,7 +666,7 @@ cudaError_t launch(const FwdParams& p, void* ws, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.g.streams * p.g.kv_heads));
+  cfg.gridDim = dim3((unsigned)(p.g.streams * p.g.kv_heads), (unsigned)(p.max_new * p.g.group));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr;

@@ -235,26 +235,24 @@ __global__ void __launch_bounds__(256) append_kernel(const Geom g, const CacheAp
   const int h = warp % g.kv_heads;
   const long long i0 = (long long)(warp / g.kv_heads) * span;
   if (i0 >= a.n_tokens) return;
+  // lane j: slot of token i0 + j (a block that starts among the first `span` may go on past them)
   const int n_slots = g.pages << g.page_shift;
-  const int i1 = (int)min((long long)a.n_tokens, i0 + span);
-  for (int i = (int)i0; i < i1;) {
-    const int slot = a.slots[i];
-    const bool ok = slot >= 0 && slot < n_slots;
-    // the block belongs to the first of its new tokens
-    const int before = i > 0 ? a.slots[i - 1] : -1;
-    if (!ok || (before >= 0 && before < n_slots && before + 1 == slot && (slot & 15) != 0)) {
-      ++i;
-      continue;
-    }
+  auto slot_at = [&](long long i) {
+    const int x = i >= 0 && i < a.n_tokens ? __ldg(a.slots + i) : -1;
+    return x < n_slots ? x : -1;
+  };
+  const int my = slot_at(i0 + lane), before = slot_at(i0 - 1);
+  const int up = __shfl_up_sync(~0u, my, 1), prev = lane == 0 ? before : up;
+  // a block belongs to the first of its new tokens
+  uint32_t leads = __ballot_sync(~0u, lane < span && my >= 0 && !(prev >= 0 && prev + 1 == my && (my & 15) != 0));
+  for (; leads; leads &= leads - 1) {
+    const int lead = __ffs(leads) - 1;
+    const int slot = __shfl_sync(~0u, my, lead);
+    const long long i = i0 + lead;
     const int held = slot & 15;
-    // its new tokens: consecutive slots from i on
-    int n = 0;
-    {
-      const int j = lane & 15;
-      const bool mine = held + j < 16 && i + j < a.n_tokens && a.slots[i + j] == slot + j;
-      const uint32_t b = __ballot_sync(~0u, mine) & 0xffffu;
-      n = __ffs(~b) - 1;
-    }
+    // its new tokens: consecutive slots from there on
+    const bool same = lane >= lead && lane - lead + held < 16 && my == slot + lane - lead;
+    const int n = __ffs(~(__ballot_sync(~0u, same) >> lead)) - 1;
     const int page = slot >> g.page_shift, off = (slot & (g.page_tokens - 1)) - held;
     const long long row = cache_row(g, page, h, off);
     const long long sidx = row >> 4;
@@ -266,8 +264,8 @@ __global__ void __launch_bounds__(256) append_kernel(const Geom g, const CacheAp
     for (int l = 0; l < NL; ++l) {
       const int r = l * RPL + r0 - held;
       const bool in = r >= 0 && r < n;
-      kx[l] = in ? __ldg((const uint4*)(kp + (long long)(i + r) * a.k_stride)) : make_uint4(0, 0, 0, 0);
-      vx[l] = in ? __ldg((const uint4*)(vp + (long long)(i + r) * a.v_stride)) : make_uint4(0, 0, 0, 0);
+      kx[l] = in ? __ldg((const uint4*)(kp + (i + r) * a.k_stride)) : make_uint4(0, 0, 0, 0);
+      vx[l] = in ? __ldg((const uint4*)(vp + (i + r) * a.v_stride)) : make_uint4(0, 0, 0, 0);
     }
     uint32_t km = 0, vm = 0, poison = 0;
 #pragma unroll
@@ -345,7 +343,6 @@ __global__ void __launch_bounds__(256) append_kernel(const Geom g, const CacheAp
       store(kx[l], (uint8_t*)a.kc, r, ke, ke_old, bad, false);
       store(vx[l], (uint8_t*)a.vc, r, ve, ve_old, false, bad);
     }
-    i += n;
   }
 }
 
@@ -362,8 +359,12 @@ cudaError_t launch_cache_plan(const cache::Geom& g, const CachePlanArgs& a, cuda
 
 cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, cudaStream_t st) {
   using namespace cache;
-  // tokens a warp looks through for blocks to take
-  const int span = 1;
+  // Tokens a warp looks through for blocks to take.  16: one warp a block of a
+  // long run of tokens, where 1 would start 15 idle warps for each that works
+  // (two 1080p frames, 24 heads of 128: 85 us against 182); 1: blocks of single
+  // tokens side by side instead of one after the other, as long as 16 would
+  // leave the GPU short of warps.
+  const int span = (long long)a.n_tokens / 16 * g.kv_heads >= 148 * 16 ? 16 : 1;
   const long long warps = (long long)((a.n_tokens + span - 1) / span) * g.kv_heads;
   const long long blocks = (warps + 7) / 8;
   if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
