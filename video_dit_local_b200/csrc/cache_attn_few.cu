@@ -254,27 +254,23 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
     // steps of this warp: keys sp.base + (k * WARPS + warp) * STEP, k in [k0, k1)
     const int* table = p.table + (long long)s * g.width;
     auto step_key = [&](int k) { return sp.base + (k * WARPS + warp) * STEP; };
-    // page of the 16 keys from `key` on; -1: none of them is to be read
-    auto page_at = [&](int key) {
-      if (key >= max_hi || key + SCALE_TOKENS <= min_lo) return -1;
-      const int pg = __ldg(table + (key >> g.page_shift));
-      if ((unsigned)pg >= (unsigned)g.pages) {
-        report_error(p.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
-        return -1;
-      }
-      return pg;
-    };
-    int pg0 = -1, pg1 = -1;  // pages of the next step to be loaded
+    // Pages of the two 16-key halves of the next step to be loaded, as read from the table (-1: none of its keys
+    // is to be read).  They are looked at only when that step is loaded, a step later, so that no warp waits here.
+    int raw0 = -1, raw1 = -1;
     auto fetch_pages = [&](int k) {
-      if (k < k1) {
-        pg0 = page_at(step_key(k));
-        pg1 = page_at(step_key(k) + SCALE_TOKENS);
-      }
+      if (k >= k1) return;
+      const int a = step_key(k), b = a + SCALE_TOKENS;
+      raw0 = a < max_hi && b > min_lo ? __ldg(table + (a >> g.page_shift)) : -1;
+      raw1 = b < max_hi && b + SCALE_TOKENS > min_lo ? __ldg(table + (b >> g.page_shift)) : -1;
     };
     auto load = [&](int k) {
       if (k < k1) {
         const int key0 = step_key(k);
         const uint32_t dst = ring + ((k - k0) % R::STAGES) * R::STAGE;
+        const int pg0 = raw0 < g.pages ? raw0 : -1, pg1 = raw1 < g.pages ? raw1 : -1;
+        if ((pg0 < 0 && key0 < max_hi && key0 + SCALE_TOKENS > min_lo) ||
+            (pg1 < 0 && key0 + SCALE_TOKENS < max_hi && key0 + STEP > min_lo))
+          report_error(p.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
         const long long row0 = cache_row(g, max(pg0, 0), h, key0 & (g.page_tokens - 1));
         const long long row1 = cache_row(g, max(pg1, 0), h, (key0 + SCALE_TOKENS) & (g.page_tokens - 1));
         constexpr int CH = D / 16, RP = 32 / CH;
@@ -299,13 +295,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       }
       cp_commit();
     };
-    fetch_pages(k0);
-#pragma unroll
-    for (int i = 0; i < R::STAGES - 1; ++i) {
-      load(k0 + i);
-      fetch_pages(k0 + i + 1);
-    }
-
     // query rows fg (+ 8) as f16 MMA fragments, each row scaled by a power of two; then what belongs to
     // the rows 2 ft, 2 ft + 1 (+ 8) whose scores this lane holds
     uint32_t qf[NT][KS][2];
@@ -318,13 +307,26 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       const int tok = in ? r / g.group : 0;
       const __nv_bfloat16* src = p.q + (long long)(sp.st.row0 + tok) * p.q_stride +
                                  (long long)(h * g.group + (in ? r - tok * g.group : 0)) * D;
-      uint2 w[KS];
-      uint32_t m = 0;
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
-        w[kk] = in ? __ldg((const uint2*)(src + (kk >> 2) * 64 + 16 * ft + 4 * (kk & 3))) : make_uint2(0, 0);
-        m = __vmaxu2(m, __vmaxu2(w[kk].x & 0x7fff7fffu, w[kk].y & 0x7fff7fffu));
+        const uint2 w = in ? __ldg((const uint2*)(src + (kk >> 2) * 64 + 16 * ft + 4 * (kk & 3))) : make_uint2(0, 0);
+        qf[u][kk][0] = w.x;
+        qf[u][kk][1] = w.y;
       }
+    }
+    // the first keys are on their way before the rows are needed
+    fetch_pages(k0);
+#pragma unroll
+    for (int i = 0; i < R::STAGES - 1; ++i) {
+      load(k0 + i);
+      fetch_pages(k0 + i + 1);
+    }
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk)
+        m = __vmaxu2(m, __vmaxu2(qf[u][kk][0] & 0x7fff7fffu, qf[u][kk][1] & 0x7fff7fffu));
       m = max(m & 0xffffu, m >> 16);
       m = max(m, __shfl_xor_sync(~0u, m, 1));
       m = max(m, __shfl_xor_sync(~0u, m, 2));
@@ -334,8 +336,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       const float down = p.scale_log2 * __int_as_float((127 - sh) << 23);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
-        qf[u][kk][0] = pack_f16(bf16lo(w[kk].x) * up, bf16hi(w[kk].x) * up);
-        qf[u][kk][1] = pack_f16(bf16lo(w[kk].y) * up, bf16hi(w[kk].y) * up);
+        qf[u][kk][0] = pack_f16(bf16lo(qf[u][kk][0]) * up, bf16hi(qf[u][kk][0]) * up);
+        qf[u][kk][1] = pack_f16(bf16lo(qf[u][kk][1]) * up, bf16hi(qf[u][kk][1]) * up);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
