@@ -66,6 +66,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
   const int n = ok ? 16 : 0;  // 0: the 16 bytes become zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
   const int n = ok ? 4 : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -274,18 +277,27 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
         const long long row0 = cache_row(g, max(pg0, 0), h, key0 & (g.page_tokens - 1));
         const long long row1 = cache_row(g, max(pg1, 0), h, (key0 + SCALE_TOKENS) & (g.page_tokens - 1));
         constexpr int CH = D / 16, RP = 32 / CH;
-        const int c = lane % CH;
-        const bool whole = pg0 >= 0 && pg1 >= 0 && key0 >= min_lo && key0 + STEP <= max_hi;
-        const long long off0 = row0 * D + (lane / CH) * D + c * 16, off1 = row1 * D + (lane / CH) * D + c * 16;
+        const int c = lane % CH, r0 = lane / CH;
+        const long long off0 = row0 * D + r0 * D + c * 16, off1 = row1 * D + r0 * D + c * 16;
+        if (pg0 >= 0 && pg1 >= 0 && key0 >= min_lo && key0 + STEP <= max_hi) {
+          const uint8_t *k_a = p.kc + off0, *k_b = p.kc + off1, *v_a = p.vc + off0, *v_b = p.vc + off1;
 #pragma unroll
-        for (int i = 0; i < STEP / RP; ++i) {
-          const int r = i * RP + lane / CH;
-          const bool second = i * RP >= SCALE_TOKENS;
-          bool in = true;
-          if (!whole) in = (second ? pg1 : pg0) >= 0 && key0 + r < max_hi && key0 + r >= min_lo;
-          const long long off = in ? (second ? off1 : off0) + (i * RP % SCALE_TOKENS) * D : 0;
-          cp16(dst + k_at<D>(r, c), p.kc + off, in);
-          cp16(dst + R::HALF + v_at<D>(r, c), p.vc + off, in);
+          for (int i = 0; i < STEP / RP; ++i) {
+            const bool second = i * RP >= SCALE_TOKENS;
+            const int at = (i * RP % SCALE_TOKENS) * D;
+            cp16(dst + k_at<D>(i * RP + r0, c), (second ? k_b : k_a) + at);
+            cp16(dst + R::HALF + v_at<D>(i * RP + r0, c), (second ? v_b : v_a) + at);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < STEP / RP; ++i) {
+            const int r = i * RP + r0;
+            const bool second = i * RP >= SCALE_TOKENS;
+            const bool in = (second ? pg1 : pg0) >= 0 && key0 + r < max_hi && key0 + r >= min_lo;
+            const long long off = in ? (second ? off1 : off0) + (i * RP % SCALE_TOKENS) * D : 0;
+            cp16(dst + k_at<D>(r, c), p.kc + off, in);
+            cp16(dst + R::HALF + v_at<D>(r, c), p.vc + off, in);
+          }
         }
         if (lane < 4) {
           const bool in = (lane & 1 ? pg1 : pg0) >= 0;
@@ -382,9 +394,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
             const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, e[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t f[4] = {
-                  e4m3x2_to_f16x2((uint16_t)(a[i] & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(e[i] & 0xffffu)),
-                  e4m3x2_to_f16x2((uint16_t)(a[i] >> 16)), e4m3x2_to_f16x2((uint16_t)(e[i] >> 16))};
+              uint32_t f[4];
+              e4m3x4_to_f16x2(a[i], f[0], f[2]);
+              e4m3x4_to_f16x2(e[i], f[1], f[3]);
 #pragma unroll
               for (int u = 0; u < NT; ++u) mma16816(sc[u][b], f, qf[u][c * 4 + i][0], qf[u][c * 4 + i][1]);
             }
@@ -406,21 +418,29 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
         for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[u][e] = -INFINITY;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const float f = fmaxf(c_row[u][e] * kf[b], 1.17549435e-38f), off = ev[b] + poison[u][e];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float v = fmaf(sc[u][b][2 * i + e], f, off);
-                if (!whole) {
-                  const int key = key0 + 16 * b + fg + 8 * i;
-                  if (key < lo[u][e] || key >= hi[u][e]) v = -INFINITY;
-                }
-                sc[u][b][2 * i + e] = v;
-                mx[u][e] = fmaxf(mx[u][e], v);
-              }
+              for (int i = 0; i < 2; ++i) sc[u][b][2 * i + e] = fmaf(sc[u][b][2 * i + e], f, off);
             }
+          }
+        if (!whole) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key0 + 8 * i + fg;
+                if (key < lo[u][e] || key >= hi[u][e]) sc[u][i >> 1][2 * (i & 1) + e] = -INFINITY;
+              }
+        }
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[u][e] = fmaxf(fmaxf(sc[u][0][e], sc[u][0][2 + e]), fmaxf(sc[u][1][e], sc[u][1][2 + e]));
             over = over || mx[u][e] > m_run[u][e] + RESCALE;
           }
         if (__any_sync(~0u, over)) {
@@ -484,10 +504,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
             // four keys' bytes of four channels -> key pairs of each channel
             const uint32_t a0 = __byte_perm(w[0][q4], w[1][q4], 0x5140), a1 = __byte_perm(w[0][q4], w[1][q4], 0x7362);
             const uint32_t b0 = __byte_perm(w[2][q4], w[3][q4], 0x5140), b1 = __byte_perm(w[2][q4], w[3][q4], 0x7362);
-            const uint32_t f0[4] = {e4m3x2_to_f16x2((uint16_t)(a0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(a0 >> 16)),
-                                    e4m3x2_to_f16x2((uint16_t)(b0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b0 >> 16))};
-            const uint32_t f1[4] = {e4m3x2_to_f16x2((uint16_t)(a1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(a1 >> 16)),
-                                    e4m3x2_to_f16x2((uint16_t)(b1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(b1 >> 16))};
+            uint32_t f0[4], f1[4];
+            e4m3x4_to_f16x2(a0, f0[0], f0[1]);
+            e4m3x4_to_f16x2(b0, f0[2], f0[3]);
+            e4m3x4_to_f16x2(a1, f1[0], f1[1]);
+            e4m3x4_to_f16x2(b1, f1[2], f1[3]);
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
               mma16816(o[u][q4 * 2], f0, pf[u][b][0], pf[u][b][1]);

@@ -304,10 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
         uint32_t out[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          out[2 * u] = e4m3x2_to_f16x2((uint16_t)(in[u] & 0xffffu));
-          out[2 * u + 1] = e4m3x2_to_f16x2((uint16_t)(in[u] >> 16));
-        }
+        for (int u = 0; u < 4; ++u) e4m3x4_to_f16x2(in[u], out[2 * u], out[2 * u + 1]);
         // 16 channels: two 16-byte chunks of the row's 128-byte box
         const int at = (2 * (c & 3)) ^ (r & 7);
         *(uint4*)(dst + r * 128 + (at << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
