@@ -413,8 +413,9 @@ enum {
  *     the stream ends, its pages return to the pool and its length becomes 0);
  *   kv_lens int32 [streams]: tokens held before; block_table: extended in place;
  *   free_pages int32 [pages], n_free int32 [1]: stack of free pages, top at
- *     n_free - 1.  Pages of ending streams are pushed first, in stream order,
- *     then pages are popped in stream order, so the result is deterministic.
+ *     n_free - 1, entries above it scratch.  Pages of ending streams are pushed
+ *     first, in stream order, then pages are popped in stream order, so the
+ *     result is deterministic.
  * Outputs: kv_lens_out [streams] (may be kv_lens) and n_free_out [1] (may be
  * n_free); q_starts int32 [streams + 1], the running sum of the new tokens;
  * slots int32 [max_tokens], -1 past the last new token; result int32 [4] =

@@ -73,7 +73,8 @@ class Planner:
             assert self.starts.tolist() == starts
             assert self.slots.tolist() == slots
             assert np.array_equal(self.table.cpu().numpy(), table)
-            assert np.array_equal(self.free.cpu().numpy()[:n_free], free[:n_free])
+            top = max(n_free, 0)            # entries above the top are scratch
+            assert np.array_equal(self.free.cpu().numpy()[:top], free[:top])
         self.host = dict(lens=lens, table=table, free=free, n_free=n_free)
         if self.lens_out is not self.lens:
             self.lens.copy_(self.lens_out)
@@ -697,3 +698,15 @@ def test_bounded_waits_run_out():
     assert (o[f.n:] == 7.5).all()
     got = f.run()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("streams,top", [(3, 3000), (700, 9), (40, 150), (1500, 2)])
+def test_plan_with_slots_of_many_tokens(streams, top):
+    """More slots than the planning block lists itself."""
+    rng = random.Random(streams)
+    p = Planner(streams, 32, 200, 3000, 4500 + streams)
+    for _ in range(4):
+        new = [rng.choice([-1, 0, 1, rng.randrange(top), top // 2]) for _ in range(streams)]
+        if p.step(new):
+            assert p.step([-1] * streams) == 0
+    _status_ok(p.V)

@@ -12,54 +12,39 @@ namespace cache {
 //   free[n_free + G_s + j] = table[s][j]                (s ends, j < have)
 //   table[s][have + j] = free[n_free + G - 1 - T_s - j] (j < pages taken)
 //   slot of token t of stream s: position len + t - Q_s in its pages.
-// One thread block does the sums and the tables: it is a handful of dependent
-// reads, and one block needs no hand-over between blocks.
+// Bound by the latency of its handful of dependent reads, so one thread block
+// does it all with one scan: a thread sums a run of streams, the block scans the
+// threads' sums, and pages (and the slots of few tokens) are dealt out to all
+// threads by a search in those sums.  Slots of many tokens are a second, wide
+// kernel.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
+// Tokens whose slots the planning block lists itself: 1000 new tokens of 1000
+// streams take 6.7 us so and 8.4 us with the second kernel, 4000 tokens of 100
+// streams 8.7 and 7.2 us.
+constexpr int PLAN_SLOTS = 2048;
 
 struct StreamPlan {
-  int have, give, take, add;
+  int len, have, give, take, add;
 };
-__device__ __forceinline__ StreamPlan stream_plan(const Geom& g, int len, int n) {
+__device__ __forceinline__ StreamPlan stream_plan(const Geom& g, const CachePlanArgs& a, int s) {
   StreamPlan r;
-  r.have = (len + g.page_tokens - 1) >> g.page_shift;
+  r.len = a.kv_lens[s];
+  const int n = a.new_tokens[s];
+  r.have = (r.len + g.page_tokens - 1) >> g.page_shift;
   r.give = n < 0 ? r.have : 0;
   r.add = max(n, 0);
-  r.take = n < 0 ? 0 : ((len + r.add + g.page_tokens - 1) >> g.page_shift) - r.have;
+  r.take = n < 0 ? 0 : ((r.len + r.add + g.page_tokens - 1) >> g.page_shift) - r.have;
   return r;
 }
 
-// Exclusive block-wide sums of three values; *total the sums themselves.
-__device__ __forceinline__ int3 block_exclusive_sums(int3 v, int3* total, int3* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int3 x = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(~0u, x.x, o), b = __shfl_up_sync(~0u, x.y, o), c = __shfl_up_sync(~0u, x.z, o);
-    if (lane >= o) {
-      x.x += a;
-      x.y += b;
-      x.z += c;
-    }
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int3 before = make_int3(0, 0, 0), all = make_int3(0, 0, 0);
-  for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-    const int3 t = warp_sums[w];
-    if (w < warp) before = make_int3(before.x + t.x, before.y + t.y, before.z + t.z);
-    all = make_int3(all.x + t.x, all.y + t.y, all.z + t.z);
-  }
-  *total = all;
-  return make_int3(before.x + x.x - v.x, before.y + x.y - v.y, before.z + x.z - v.z);
-}
-
-// Last s in [0, n) with first[s] <= i (first is non-decreasing, first[0] <= i).
-__device__ __forceinline__ int last_at_most(const int* first, int n, int i) {
+// Last i in [0, n) with first[i] <= x (first is non-decreasing, first[0] <= x).
+template <class T>
+__device__ __forceinline__ int last_at_most(const T* first, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (first[mid] <= i)
+    if (first[mid] <= x)
       lo = mid;
     else
       hi = mid;
@@ -67,143 +52,187 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const CachePlanArgs a) {
-  __shared__ int3 warp_sums[PLAN_THREADS / 32];
-  __shared__ int first[PLAN_THREADS], have_s[PLAN_THREADS];
-  __shared__ unsigned long long tot_add;
-  __shared__ long long tot_give, tot_take;
-  __shared__ int worst, longest;
-  const int t = threadIdx.x;
-  const long long cap = (long long)g.width << g.page_shift;
-  if (t == 0) {
-    tot_add = 0;
-    tot_give = tot_take = 0;
-    worst = VATTN_PLAN_OK;
-    longest = 0;
-  }
-  __syncthreads();
-  const int n_free = *a.n_free;
+__device__ __forceinline__ int slot_of(const Geom& g, const int* table, int s, int pos) {
+  const int page = table[(long long)s * g.width + (pos >> g.page_shift)];
+  return (unsigned)page < (unsigned)g.pages ? (page << g.page_shift) + (pos & (g.page_tokens - 1)) : -1;
+}
 
-  // totals and the verdict, before anything is written
-  for (int s = t; s < g.streams; s += PLAN_THREADS) {
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const CachePlanArgs a, int list_slots) {
+  __shared__ long long warp_give[32], warp_take[32], warp_add[32];
+  __shared__ int warp_longest[32], warp_worst[32];
+  __shared__ int give0[PLAN_THREADS], take0[PLAN_THREADS], add0[PLAN_THREADS];
+  __shared__ int bad_page;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const long long cap = (long long)g.width << g.page_shift;
+  const int n_free = *a.n_free;
+  const int per = (g.streams + PLAN_THREADS - 1) / PLAN_THREADS;
+  const int s0 = min(t * per, g.streams), s1 = min(s0 + per, g.streams);
+  if (t == 0) bad_page = 0;
+
+  // sums and the verdict, before anything is written
+  long long give = 0, take = 0, add = 0;
+  int longest = 0, worst = VATTN_PLAN_OK;
+  for (int s = s0; s < s1; ++s) {
     const int len = a.kv_lens[s], n = a.new_tokens[s];
     if (len < 0 || len > cap) {
-      atomicMax(&worst, VATTN_PLAN_BAD_STATE);
-      continue;
+      worst = max(worst, VATTN_PLAN_BAD_STATE);
+    } else if (n >= 0 && len + (long long)n > cap) {
+      worst = max(worst, VATTN_PLAN_TABLE_FULL);
+    } else {
+      const StreamPlan r = stream_plan(g, a, s);
+      give += r.give;
+      take += r.take;
+      add += r.add;
+      longest = max(longest, n < 0 ? 0 : len + r.add);
     }
-    if (n >= 0 && len + (long long)n > cap) {
-      atomicMax(&worst, VATTN_PLAN_TABLE_FULL);
-      continue;
+  }
+  const long long my_give = give, my_take = take, my_add = add;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(~0u, give, o), y = __shfl_up_sync(~0u, take, o), z = __shfl_up_sync(~0u, add, o);
+    if (lane >= o) {
+      give += x;
+      take += y;
+      add += z;
     }
-    const StreamPlan r = stream_plan(g, len, n);
-    atomicAdd(&tot_add, (unsigned long long)r.add);
-    atomicAdd((unsigned long long*)&tot_give, (unsigned long long)r.give);
-    atomicAdd((unsigned long long*)&tot_take, (unsigned long long)r.take);
-    atomicMax(&longest, n < 0 ? 0 : len + r.add);
-    for (int j = 0; j < r.give; ++j)
-      if ((unsigned)a.table[(long long)s * g.width + j] >= (unsigned)g.pages) atomicMax(&worst, VATTN_PLAN_BAD_STATE);
+    longest = max(longest, __shfl_xor_sync(~0u, longest, o));
+    worst = max(worst, __shfl_xor_sync(~0u, worst, o));
+  }
+  if (lane == 31) {
+    warp_give[warp] = give;
+    warp_take[warp] = take;
+    warp_add[warp] = add;
+    warp_longest[warp] = longest;
+    warp_worst[warp] = worst;
   }
   __syncthreads();
+  long long tot_give, tot_take, tot_add;
+  {  // every warp scans the warps' sums
+    const long long wg = warp_give[lane], wt = warp_take[lane], wa = warp_add[lane];
+    long long sg = wg, st = wt, sa = wa;
+    longest = warp_longest[lane];
+    worst = warp_worst[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(~0u, sg, o), y = __shfl_up_sync(~0u, st, o), z = __shfl_up_sync(~0u, sa, o);
+      if (lane >= o) {
+        sg += x;
+        st += y;
+        sa += z;
+      }
+      longest = max(longest, __shfl_xor_sync(~0u, longest, o));
+      worst = max(worst, __shfl_xor_sync(~0u, worst, o));
+    }
+    tot_give = __shfl_sync(~0u, sg, 31);
+    tot_take = __shfl_sync(~0u, st, 31);
+    tot_add = __shfl_sync(~0u, sa, 31);
+    give += __shfl_sync(~0u, sg - wg, warp) - my_give;
+    take += __shfl_sync(~0u, st - wt, warp) - my_take;
+    add += __shfl_sync(~0u, sa - wa, warp) - my_add;
+  }
   int verdict = worst;
   if (verdict == VATTN_PLAN_OK) {
     if (n_free < 0 || n_free + tot_give > g.pages)
       verdict = VATTN_PLAN_BAD_STATE;
-    else if ((long long)tot_add > a.max_tokens)
+    else if (tot_add > a.max_tokens)
       verdict = VATTN_PLAN_NO_SLOTS;
     else if (tot_take > n_free + tot_give)
       verdict = VATTN_PLAN_NO_PAGES;
   }
+  // (sums that passed fit an int: at most pages, and max_tokens)
+  give0[t] = (int)give;
+  take0[t] = (int)take;
+  add0[t] = (int)add;
+  __syncthreads();
+
+  if (verdict == VATTN_PLAN_OK && tot_give > 0) {
+    // pages of ending streams onto the stack: above its top, so nothing is lost if one turns out bad
+    for (int i = t; i < (int)tot_give; i += PLAN_THREADS) {
+      const int u = last_at_most(give0, PLAN_THREADS, i);
+      int s = u * per, j = i - give0[u];
+      for (int x; j >= (x = stream_plan(g, a, s).give); ++s) j -= x;
+      const int page = a.table[(long long)s * g.width + j];
+      if ((unsigned)page >= (unsigned)g.pages) bad_page = 1;
+      a.free_pages[n_free + i] = page;
+    }
+    __syncthreads();
+    if (bad_page) verdict = VATTN_PLAN_BAD_STATE;
+  }
   if (verdict != VATTN_PLAN_OK) {
     int top = 0;
-    for (int s = t; s < g.streams; s += PLAN_THREADS) {
+    for (int s = s0; s < s1; ++s) {
       const int len = a.kv_lens[s];
       a.kv_lens_out[s] = len;
+      a.q_starts[s] = 0;
       top = max(top, len);
     }
-    for (int s = t; s <= g.streams; s += PLAN_THREADS) a.q_starts[s] = 0;
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) warp_longest[warp] = top;
     __syncthreads();
-    if (t == 0) longest = 0;
-    __syncthreads();
-    atomicMax(&longest, top);
-    __syncthreads();
+    if (list_slots)
+      for (int i = t; i < a.max_tokens; i += PLAN_THREADS) a.slots[i] = -1;
     if (t == 0) {
+      for (int w = 0; w < PLAN_THREADS / 32; ++w) top = max(top, warp_longest[w]);
+      a.q_starts[g.streams] = 0;
       *a.n_free_out = n_free;
       a.result[0] = verdict;
       a.result[1] = 0;
       a.result[2] = n_free;
-      a.result[3] = longest;
+      a.result[3] = top;
     }
     return;
   }
-  const int avail = n_free + (int)tot_give;
 
-  // pages of ending streams onto the stack
-  if (tot_give > 0) {
-    int base = n_free;
-    for (int s0 = 0; s0 < g.streams; s0 += PLAN_THREADS) {
-      const int s = s0 + t;
-      int give = 0;
-      if (s < g.streams) give = stream_plan(g, a.kv_lens[s], a.new_tokens[s]).give;
-      int3 all;
-      const int3 ex = block_exclusive_sums(make_int3(give, 0, 0), &all, warp_sums);
-      first[t] = ex.x;
-      __syncthreads();
-      for (int i = t; i < all.x; i += PLAN_THREADS) {
-        const int u = last_at_most(first, PLAN_THREADS, i);
-        a.free_pages[base + i] = a.table[(long long)(s0 + u) * g.width + (i - first[u])];
-      }
-      base += all.x;
-      __syncthreads();
-    }
+  // new pages off the stack
+  const int avail = n_free + (int)tot_give;
+  for (int i = t; i < (int)tot_take; i += PLAN_THREADS) {
+    const int u = last_at_most(take0, PLAN_THREADS, i);
+    int s = u * per, j = i - take0[u];
+    for (int x; j >= (x = stream_plan(g, a, s).take); ++s) j -= x;
+    a.table[(long long)s * g.width + stream_plan(g, a, s).have + j] = a.free_pages[avail - 1 - i];
   }
-  // new pages off the stack, lengths and token ranges
-  int taken = 0, token0 = 0;
-  for (int s0 = 0; s0 < g.streams; s0 += PLAN_THREADS) {
-    const int s = s0 + t;
-    StreamPlan r = {0, 0, 0, 0};
-    int len = 0, n = 0;
-    if (s < g.streams) {
-      len = a.kv_lens[s];
-      n = a.new_tokens[s];
-      r = stream_plan(g, len, n);
-    }
-    int3 all;
-    const int3 ex = block_exclusive_sums(make_int3(r.take, r.add, 0), &all, warp_sums);
-    first[t] = ex.x;
-    have_s[t] = r.have;
-    if (s < g.streams) {
-      a.q_starts[s] = token0 + ex.y;
-      a.kv_lens_out[s] = n < 0 ? 0 : len + r.add;
+  __syncthreads();
+  // slots, from the lengths before the step
+  if (list_slots) {
+    for (int i = t; i < a.max_tokens; i += PLAN_THREADS) {
+      int slot = -1;
+      if (i < (int)tot_add) {
+        const int u = last_at_most(add0, PLAN_THREADS, i);
+        int s = u * per, j = i - add0[u];
+        for (int x; j >= (x = stream_plan(g, a, s).add); ++s) j -= x;
+        slot = slot_of(g, a.table, s, a.kv_lens[s] + j);
+      }
+      a.slots[i] = slot;
     }
     __syncthreads();
-    for (int i = t; i < all.x; i += PLAN_THREADS) {
-      const int u = last_at_most(first, PLAN_THREADS, i);
-      a.table[(long long)(s0 + u) * g.width + have_s[u] + (i - first[u])] = a.free_pages[avail - 1 - taken - i];
-    }
-    taken += all.x;
-    token0 += all.y;
-    __syncthreads();
+  }
+  // the lengths may be updated in place: last
+  int q = (int)add;
+  for (int s = s0; s < s1; ++s) {
+    const StreamPlan r = stream_plan(g, a, s);
+    const int n = a.new_tokens[s];
+    a.q_starts[s] = q;
+    a.kv_lens_out[s] = n < 0 ? 0 : r.len + r.add;
+    q += r.add;
   }
   if (t == 0) {
-    a.q_starts[g.streams] = token0;
-    *a.n_free_out = avail - taken;
+    a.q_starts[g.streams] = (int)tot_add;
+    *a.n_free_out = avail - (int)tot_take;
     a.result[0] = VATTN_PLAN_OK;
-    a.result[1] = token0;
-    a.result[2] = avail - taken;
+    a.result[1] = (int)tot_add;
+    a.result[2] = avail - (int)tot_take;
     a.result[3] = longest;
   }
 }
 
-// Slots of the new tokens, from the tables that plan_kernel left.
+// Slots of many new tokens, from the tables and lengths that plan_kernel left.
 __global__ void __launch_bounds__(256) slots_kernel(const Geom g, const CachePlanArgs a) {
   const int t = blockIdx.x * 256 + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t >= a.max_tokens) return;
   int slot = -1;
   if (t < a.q_starts[g.streams]) {
     const int s = last_at_most(a.q_starts, g.streams, t);
-    const int pos = a.kv_lens_out[s] - a.q_starts[s + 1] + t;
-    const int page = a.table[(long long)s * g.width + (pos >> g.page_shift)];
-    if ((unsigned)page < (unsigned)g.pages) slot = (page << g.page_shift) + (pos & (g.page_tokens - 1));
+    slot = slot_of(g, a.table, s, a.kv_lens_out[s] - a.q_starts[s + 1] + t);
   }
   a.slots[t] = slot;
 }
@@ -350,11 +379,20 @@ __global__ void __launch_bounds__(256) append_kernel(const Geom g, const CacheAp
 
 cudaError_t launch_cache_plan(const cache::Geom& g, const CachePlanArgs& a, cudaStream_t st) {
   using namespace cache;
-  plan_kernel<<<1, PLAN_THREADS, 0, st>>>(g, a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.max_tokens == 0) return e;
-  slots_kernel<<<(a.max_tokens + 255) / 256, 256, 0, st>>>(g, a);
-  return cudaGetLastError();
+  const bool few = a.max_tokens <= PLAN_SLOTS;
+  plan_kernel<<<1, PLAN_THREADS, 0, st>>>(g, a, few ? 1 : 0);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || few) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.max_tokens + 255) / 256);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, slots_kernel, g, a);
 }
 
 cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, cudaStream_t st) {
