@@ -79,10 +79,36 @@ struct Smem {
 struct Params {
   FwdParams f;
   int q_tiles;   // tiles of rows (of all of a thread block's) that a stream can have
-  int splits;    // thread blocks that share a tile's keys
-  float* part;   // splits > 1: partial results [stream][kv head][tile][split][row][d], then (m, l) pairs
+  int whole;     // items (a tile of rows, kv head and stream) with a thread block each
+  int splits;    // thread blocks that share the keys of each of the other items
+  int tile_slow; // order of the items: streams, kv heads, tiles (0) or tiles, streams, kv heads (1)
+  float* part;   // partial results [item - whole][split][row][d], then (m, l) pairs
   float2* part_ml;
 };
+
+// Item -> tile, kv head, stream.  Later tiles see more keys under a causal
+// mask: they come first.
+struct Item {
+  int tile, h, s;
+};
+__device__ __forceinline__ Item item_of(const Params& pp, int item) {
+  const Geom& g = pp.f.g;
+  Item r;
+  int rest;
+  if (pp.tile_slow) {
+    rest = item;
+    const int per_tile = g.streams * g.kv_heads;
+    r.tile = rest / per_tile;
+    rest -= r.tile * per_tile;
+  } else {
+    rest = item / pp.q_tiles;
+    r.tile = item - rest * pp.q_tiles;
+  }
+  r.tile = pp.q_tiles - 1 - r.tile;
+  r.s = rest / g.kv_heads;
+  r.h = rest - r.s * g.kv_heads;
+  return r;
+}
 
 // Instruction descriptor, kind::f16, f16 x f16 -> f32, B MN-major (V rows are keys).
 constexpr uint32_t idesc_f16_pv(int N) {
@@ -131,21 +157,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int ROWS = L::TILES * BM;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const FwdParams& p = pp.f;
   const Geom& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // what this block computes; later tiles see more keys under a causal mask, so they go first
-  const int split = blockIdx.x % pp.splits;
-  const int tile = pp.q_tiles - 1 - blockIdx.x / pp.splits;
-  const int h = blockIdx.y, s = blockIdx.z;
+  // what this block computes
+  const int spare = (int)blockIdx.x - pp.whole;
+  const bool whole = spare < 0;
+  const int shared = whole ? 0 : spare / pp.splits;
+  const int splits = whole ? 1 : pp.splits, split = whole ? 0 : spare - shared * pp.splits;
+  const Item it = item_of(pp, whole ? (int)blockIdx.x : pp.whole + shared);
+  const int tile = it.tile, h = it.h, s = it.s;
   const StreamStep st = stream_step(p, s);
   const int row0 = tile * ROWS;
   const int rows = min(ROWS, st.n * g.group - row0);
   if (rows <= 0) return;
   const TileKeys tk = tile_keys(g, st, row0, rows);
-  const int b0 = tk.first + (int)((long long)tk.count * split / pp.splits);
-  const int nblk = tk.first + (int)((long long)tk.count * (split + 1) / pp.splits) - b0;
+  const int b0 = tk.first + (int)((long long)tk.count * split / splits);
+  const int nblk = tk.first + (int)((long long)tk.count * (split + 1) / splits) - b0;
   if (nblk == 0) {
     // no keys here: rows that see none at all are written by the first split, the join skips the rest
     if (tk.count == 0 && split == 0) {
@@ -382,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int tok = real ? (row0 + brow) / g.group : 0;
     const int head = h * g.group + (real ? row0 + brow - tok * g.group : 0);
     const size_t out_row = (size_t)(st.row0 + tok) * g.q_heads + head;
-    int lo = 0, hi = 0;
+    int lo = 0, hi = 0x7fffffff;  // rows that do not exist mask nothing, and are not written
     if (real) key_range(g, st, tok, &lo, &hi);
     // the query row, scaled and split into hi + lo, in the MMA's layout.  One tile: the groups take half a row each.
     float c_row, poison;
@@ -548,13 +578,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         a1 = w == 0 ? a_other : a_self;
         both = nblk >= 2;
       }
-      const bool whole = pp.splits == 1;
       const float norm = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
       a0 *= norm;
       a1 *= norm;
       const uint32_t t0 = TWO ? tO : tmem + lane_addr + 256u, t1 = tmem + lane_addr + 384u;
-      const size_t pr =
-          whole ? 0 : ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + split) * ROWS + brow;
+      const size_t pr = ((size_t)shared * splits + split) * ROWS + brow;
       constexpr int SPAN = TWO ? D : D / 2;
 #pragma unroll
       for (int c = 0; c < SPAN; c += 32) {
@@ -596,35 +624,41 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins the splits of each row, in their order; one warp a row.
+// Joins the splits of each row of the shared items, in their order; one warp a row.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const Params pp, int tile_rows) {
   const FwdParams& p = pp.f;
   const Geom& g = p.g;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int h = blockIdx.y, s = blockIdx.z;
-  const StreamStep st = stream_step(p, s);
-  const int all = st.n * g.group;
-  if (r >= all) return;
-  const int tile = r / tile_rows, row = r % tile_rows;
-  const TileKeys tk = tile_keys(g, st, tile * tile_rows, min(tile_rows, all - tile * tile_rows));
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const Item it = item_of(pp, pp.whole + blockIdx.x);
+  const StreamStep st = stream_step(p, it.s);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int rows = min(tile_rows, st.n * g.group - it.tile * tile_rows);
+  if (row >= rows) return;
+  const TileKeys tk = tile_keys(g, st, it.tile * tile_rows, rows);
   if (tk.count == 0) return;
   constexpr int PER = D / 32;
   float acc[PER] = {};
   float m = -INFINITY, l = 0.f;
+#pragma unroll 2
   for (int i = 0; i < pp.splits; ++i) {
     if ((long long)tk.count * i / pp.splits == (long long)tk.count * (i + 1) / pp.splits) continue;
-    const size_t pr = ((((size_t)s * g.kv_heads + h) * pp.q_tiles + tile) * pp.splits + i) * tile_rows + row;
-    const float2 ml = pp.part_ml[pr];
+    const size_t pr = ((size_t)blockIdx.x * pp.splits + i) * tile_rows + row;
+    const float2 ml = __ldcg(pp.part_ml + pr);
+    float v[PER];
+#pragma unroll
+    for (int c = 0; c < PER; c += 2)
+      *(float2*)(v + c) = __ldcg((const float2*)(pp.part + pr * D + lane * PER + c));
     const float m_new = fmaxf(m, ml.x), ref = m_new == -INFINITY ? 0.f : m_new;
     const float a = ex2(m - ref), e = ex2(ml.x - ref);
     l = l * a + ml.y * e;
 #pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = acc[c] * a + pp.part[pr * D + lane * PER + c] * e;
+    for (int c = 0; c < PER; ++c) acc[c] = acc[c] * a + v[c] * e;
     m = m_new;
   }
+  const int r = it.tile * tile_rows + row;
   const int tok = r / g.group;
-  const size_t at = (size_t)(st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+  const size_t at = (size_t)(st.row0 + tok) * g.q_heads + it.h * g.group + (r - tok * g.group);
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int c = 0; c < PER; c += 2)
@@ -639,32 +673,65 @@ int tiles_of(const Geom& g, long long max_new) {
   return (int)((max_new * g.group + rows - 1) / rows);
 }
 
-// Thread blocks that share a tile's keys: what makes the waves of 148 thread
-// blocks fullest, each split costing 2% of a tile for its start and the join.
-int splits_of(const Geom& g, long long max_new) {
-  const long long items = (long long)g.streams * g.kv_heads * tiles_of(g, max_new);
-  int best = 1;
-  double least = 1e30;
-  for (int sp = 1; sp <= 32 && items * sp <= 148 * 8; ++sp) {
-    const double cost = (double)((items * sp + 147) / 148) / sp * (1 + 0.02 * (sp - 1));
+// How the items are dealt out.  In units of a key block, a thread block costs
+// its keys and about 3 for its start and end, and 3 more where partial results
+// are written and joined; the cache's capacity stands in for the streams'
+// lengths, which the host does not know.
+//  - Streams alike (one stream, every query sees every key): as many items as
+//    fill whole waves of the 148 SMs get a thread block each, the rest are
+//    split into equal shares that fill the last waves.
+//  - Else all items get the same number of splits: enough that the last ones
+//    to finish are short, counting half the tiles as there.
+struct Deal {
+  long long items, whole;
+  int splits;
+};
+Deal deal(const Geom& g, long long max_new) {
+  constexpr int SMS = 148, MOST = SMS * 8;  // MOST bounds the partial results
+  Deal d;
+  d.items = (long long)g.streams * g.kv_heads * tiles_of(g, max_new);
+  d.whole = d.items;
+  d.splits = 1;
+  const double blocks = std::max(1.0, (double)g.width * g.page_tokens / BN);
+  double least = 1e300;
+  auto take = [&](long long whole, int splits, double cost) {
     if (cost < least) {
       least = cost;
-      best = sp;
+      d.whole = splits == 1 ? d.items : whole;
+      d.splits = splits;
+    }
+  };
+  if (g.streams == 1 && g.frame == 0) {
+    const long long waves = d.items / SMS;
+    for (long long w = std::max(0ll, waves - 2); w <= waves; ++w) {
+      const long long rest = d.items - w * SMS;
+      for (int sp = 1; sp == 1 || (sp <= 64 && rest * sp <= MOST); ++sp)
+        take(w * SMS, sp, w * (blocks + 3) + (double)((rest * sp + SMS - 1) / SMS) * (blocks / sp + (sp == 1 ? 3 : 6)));
+    }
+  } else {
+    for (int sp = 1; sp == 1 || (sp <= 64 && d.items * sp <= MOST); ++sp) {
+      const double each = blocks / sp + (sp == 1 ? 3 : 6);
+      take(0, sp, std::max(1.0, 0.5 * d.items * sp / SMS) * each + each);
     }
   }
-  return best;
+  return d;
 }
 size_t part_rows(const Geom& g, long long max_new) {
-  const int sp = splits_of(g, max_new);
-  return sp == 1 ? 0 : (size_t)g.streams * g.kv_heads * tiles_of(g, max_new) * sp * rows_of(g, max_new);
+  const Deal d = deal(g, max_new);
+  return (size_t)(d.items - d.whole) * (d.splits == 1 ? 0 : d.splits) * rows_of(g, max_new);
 }
 
 template <int D, bool TWO>
 cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
+  const Deal d = deal(f.g, f.max_new);
+  const long long grid = d.whole + (d.items - d.whole) * d.splits;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
   Params p;
   p.f = f;
   p.q_tiles = tiles_of(f.g, f.max_new);
-  p.splits = splits_of(f.g, f.max_new);
+  p.whole = (int)d.whole;
+  p.splits = d.splits;
+  p.tile_slow = 0;
   p.part = (float*)ws;
   p.part_ml = (float2*)(p.part + part_rows(f.g, f.max_new) * D);
   CUtensorMap tk, tv;
@@ -677,12 +744,20 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   constexpr int smem = Smem<D, TWO>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(p.q_tiles * p.splits, f.g.kv_heads, f.g.streams), THREADS, smem, stream>>>(tk, tv, p);
+  kernel<<<(unsigned)grid, THREADS, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
-  const int rows = (int)(f.max_new * f.g.group);
-  join_kernel<D><<<dim3((rows + 7) / 8, f.g.kv_heads, f.g.streams), 256, 0, stream>>>(p, rows_of(f.g, f.max_new));
-  return cudaGetLastError();
+  if (e != cudaSuccess || d.whole == d.items) return e;
+  const int rows = rows_of(f.g, f.max_new);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(d.items - d.whole), (unsigned)(rows / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, rows);
 }
 
 }  // namespace many
