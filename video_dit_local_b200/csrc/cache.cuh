@@ -71,11 +71,14 @@ __device__ __forceinline__ void key_range(const Geom& g, const StreamStep& st, i
   *lo = 0;
   *hi = st.len;
   if (g.frame > 0) {
-    const long long pos = (long long)st.len - st.n + i;
-    const long long f = pos >= 0 ? pos / g.frame : -1;
-    const long long end = (f + 1) * g.frame;
-    *hi = (int)min((long long)st.len, end);
-    if (g.window > 0) *lo = (int)max(0ll, (f - g.window + 1) * g.frame);
+    const int pos = st.len - st.n + i;  // both below 2^31
+    if (pos < 0) {
+      *hi = 0;
+      return;
+    }
+    const unsigned from = (unsigned)pos / (unsigned)g.frame * (unsigned)g.frame;  // first of its frame
+    *hi = (int)min((unsigned)st.len, from + (unsigned)g.frame);
+    if (g.window > 0) *lo = (int)max(0ll, (long long)from - (g.window - 1ll) * g.frame);
   }
 }
 

@@ -3,17 +3,19 @@
 //
 // A thread block takes the query rows (token, query head of the group) of one
 // stream and kv head in tiles of 128 and streams the keys they see in blocks of
-// 128.  12 warps:
-//   warps 0-3 and 4-7  two softmax groups, each with an S and an O accumulator
-//                      in TMEM.  TWO = true: a tile of rows each (256 rows a
+// 128.  20 warps:
+//   warps 0-7 and 8-15 two softmax groups, each with an S and an O accumulator
+//                      in TMEM; a row's 128 scores are shared by two threads,
+//                      64 each (720p frame over ten: 1.89 ms; 1.93 with one
+//                      thread a row and half as many warps).  TWO = true: a tile of rows each (256 rows a
 //                      thread block), on the same key blocks, so that one
 //                      conversion of V serves 256 rows; false (no stream has
 //                      more than 128 rows): one tile, alternate key blocks,
 //                      joined at the end;
-//   warps 8, 9         convert V, e4m3 -> f16, from one swizzled tile into the
+//   warps 16, 17       convert V, e4m3 -> f16, from one swizzled tile into the
 //                      other that P V reads;
-//   warp 10            K and V pages by TMA, and the blocks' scales;
-//   warp 11            issues the MMAs and owns the TMEM allocation.
+//   warp 18            K and V pages by TMA, and the blocks' scales;
+//   warp 19            issues the MMAs and owns the TMEM allocation.
 //
 // Q K^T runs on the cached bytes as they are (kind::f8f6f4).  A bf16 query has
 // 8 significant bits, an e4m3 value 4: each row is scaled by a power of two
@@ -41,8 +43,8 @@ using fwd::idesc_e4m3_f32;
 using fwd::mma_ss_e4m3;
 
 constexpr int BM = 128, BN = 128;
-constexpr int THREADS = 384;
-constexpr int WARP_V = 8, V_WARPS = 2, WARP_K = 10, WARP_MMA = 11;
+constexpr int THREADS = 640, SOFTMAX = 512;
+constexpr int WARP_V = 16, V_WARPS = 2, WARP_K = 18, WARP_MMA = 19;
 constexpr int NV = 2;   // ring stages of V as f16
 // Scale ring: block j + 8 is written after Q K^T of block j + 5 (or j + 6) is
 // done, which is issued after P of block j + 2, whose group has long read block
@@ -53,7 +55,7 @@ constexpr float P_SHIFT = 7.0f;
 constexpr int SUBS = BN / SCALE_TOKENS;
 
 // Of each 16 keys of a block: K's scale, log2 of V's, and 2^-log2 of V's.
-struct Scales {
+struct alignas(16) Scales {
   float k[SUBS], e[SUBS], inv[SUBS];
 };
 
@@ -69,8 +71,8 @@ struct Smem {
   static constexpr int OFF_V = OFF_V8 + NK * QK;
   static constexpr int OFF_SC = OFF_V + NV * V;              // NS x Scales
   static constexpr int OFF_XCH = OFF_SC + NS * (int)sizeof(Scales);
-  static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
-  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 1 + NS;
+  static constexpr int OFF_BAR = OFF_XCH + 4 * 128 * 8;      // [group][half][row] pairs of floats
+  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 1 + NS + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int TOTAL = OFF_MISC + 16;
   static constexpr int ALLOC = TOTAL + 1024;
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* p_full = s_full + 2;     // ... and its P
   uint64_t* o_final = p_full + 2;
   uint64_t* sc_full = o_final + 1;
+  uint64_t* max_full = sc_full + NS;  // [group][quad]: both halves of the rows' maxima are there
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   float2* xch = reinterpret_cast<float2*>(smem + L::OFF_XCH);
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   wc.err_word = p.ctl.err_word;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 256);
+    mbar_init(q_full, SOFTMAX);
     for (int i = 0; i < NK; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -222,8 +225,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&max_full[i], 2);
     mbar_init(o_final, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&sc_full[i], 1);
     *abort_flag = 0;
@@ -405,49 +409,46 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ---------------- softmax groups ----------------
-    const int w = warp >> 2, quad = warp & 3;
+    const int w = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
     const int row = quad * 32 + lane;                    // in its tile
     const int brow = (TWO ? w * BM : 0) + row;           // in the thread block's rows
     const bool real = brow < rows;
+    // none of the warp's rows exists: it leaves P as it finds it, in rows that nobody reads
+    const bool idle = brow - lane >= rows;
     const int tok = real ? (row0 + brow) / g.group : 0;
-    const int head = h * g.group + (real ? row0 + brow - tok * g.group : 0);
-    const size_t out_row = (size_t)(st.row0 + tok) * g.q_heads + head;
+    const size_t out_row =
+        (size_t)(st.row0 + tok) * g.q_heads + h * g.group + (real ? row0 + brow - tok * g.group : 0);
     int lo = 0, hi = 0x7fffffff;  // rows that do not exist mask nothing, and are not written
     if (real) key_range(g, st, tok, &lo, &hi);
-    // the query row, scaled and split into hi + lo, in the MMA's layout.  One tile: the groups take half a row each.
+    // the query rows, scaled and split into hi + lo, in the MMA's layout: a warp takes ROWS / 16 of them, 16 bytes
+    // of bf16 a lane; the rows' factors and non-finite marks go through shared memory to the lanes that need them
     float c_row, poison;
     {
-      constexpr int NC = TWO ? D / 16 : D / 32;  // 16-element chunks a thread
-      const int first = TWO ? 0 : w * NC;
-      uint8_t* q_hi = smem + L::OFF_Q + (TWO ? w : 0) * 2 * L::QK;
-      uint4 x[2 * NC];
-      uint32_t m = 0;
-      const uint4* src =
-          (const uint4*)(p.q + (long long)(st.row0 + tok) * p.q_stride + (long long)head * D + first * 16);
+      constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = ROWS / 16 / RPI;
+      const int c = lane % LPR;
+      uint4 x[ITERS];
 #pragma unroll
-      for (int i = 0; i < 2 * NC; ++i) {
-        x[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      for (int i = 0; i < ITERS; ++i) {
+        const int r = warp * (ROWS / 16) + i * RPI + lane / LPR;
+        const int t = r < rows ? (row0 + r) / g.group : 0;
+        x[i] = r < rows ? __ldg((const uint4*)(p.q + (long long)(st.row0 + t) * p.q_stride +
+                                               (long long)(h * g.group + row0 + r - t * g.group) * D) + c)
+                        : make_uint4(0, 0, 0, 0);
       }
-      m = max(m & 0xffffu, m >> 16);
-      if constexpr (!TWO) {
-        xch[w * 128 + row].x = __uint_as_float(m);
-        named_bar_sync(1, 256);
-        m = max(m, __float_as_uint(xch[(1 - w) * 128 + row].x));
-        named_bar_sync(1, 256);
-      }
-      poison = m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
-      const int sh = m == 0 ? 0 : min(7 - ((int)(m >> 7) - 127), 126);
-      const float up = __int_as_float((sh + 127) << 23);
-      c_row = p.scale_log2 * __int_as_float((127 - sh) << 23);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        uint32_t hv[4], lv[4];
-        const uint32_t in[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
-                                x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+      for (int i = 0; i < ITERS; ++i) {
+        const int r = warp * (ROWS / 16) + i * RPI + lane / LPR;
+        uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                              __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+        const int sh = m == 0 ? 0 : min(7 - ((int)(m >> 7) - 127), 126);
+        const float up = __int_as_float((sh + 127) << 23);
+        uint32_t hv[2], lv[2];
+        const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           uint32_t hh[2], ll[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -459,16 +460,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           hv[u] = hh[0] | (hh[1] << 16);
           lv[u] = ll[0] | (ll[1] << 16);
         }
-        const uint32_t at = byte_chunk<D>(row, first + i);
-        *(uint4*)(q_hi + at) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *(uint4*)(q_hi + L::QK + at) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
+        uint8_t* at = smem + L::OFF_Q + (r >> 7) * 2 * L::QK + byte_chunk<D>(r & 127, c >> 1) + (c & 1) * 8;
+        *(uint2*)at = make_uint2(hv[0], hv[1]);
+        *(uint2*)(at + L::QK) = make_uint2(lv[0], lv[1]);
+        if (c == 0)
+          xch[r] = make_float2(p.scale_log2 * __int_as_float((127 - sh) << 23),
+                               m >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f);
       }
       fence_async_smem();
       mbar_arrive(q_full);
+      named_bar_sync(1, SOFTMAX);
+      c_row = xch[brow].x;
+      poison = xch[brow].y;
+      named_bar_sync(1, SOFTMAX);
     }
     const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lane_addr + (uint32_t)(w * 128);
     const uint32_t tO = tmem + lane_addr + 256u + (uint32_t)(w * 128);
+    float* my_max = (float*)xch + (w * 2 + half) * 256 + row;          // two slots, 128 floats apart
+    const float* other_max = (float*)xch + (w * 2 + 1 - half) * 256 + row;
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
     for (int i = 0;; ++i) {
@@ -478,25 +488,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t sr[4][32];
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(tS + q4 * 32, sr[q4]);
+      if (idle) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+        continue;
+      }
+      // this thread's 64 scores: keys 64 half .. of the block
+      uint32_t sr[2][32];
+      tmem_ld32(tS + half * 64, sr[0]);
+      tmem_ld32(tS + half * 64 + 32, sr[1]);
       // x = S f + e for each 16 keys; f > 0, so that a masked score stays -inf
-      const Scales& sc = scales[j % NS];
-      auto factor = [&](int b) { return fmaxf(c_row * sc.k[b], 1.17549435e-38f); };
-      auto offset = [&](int b) { return sc.e[b] + poison; };
+      const float4 k4 = *(const float4*)&scales[j % NS].k[half * 4], e4 = *(const float4*)&scales[j % NS].e[half * 4];
+      const float4 i4 = *(const float4*)&scales[j % NS].inv[half * 4];
+      const float f[4] = {fmaxf(c_row * k4.x, 1.17549435e-38f), fmaxf(c_row * k4.y, 1.17549435e-38f),
+                          fmaxf(c_row * k4.z, 1.17549435e-38f), fmaxf(c_row * k4.w, 1.17549435e-38f)};
+      const float e[4] = {e4.x, e4.y, e4.z, e4.w}, inv[4] = {i4.x, i4.y, i4.z, i4.w};
       tmem_wait_ld();
-      const int from = lo - (b0 + j) * BN, to = hi - (b0 + j) * BN;
-      if (from > 0 || to < BN) {
+      const int from = lo - (b0 + j) * BN - half * 64, to = hi - (b0 + j) * BN - half * 64;
+      if (from > 0 || to < BN / 2) {
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4)
+        for (int q2 = 0; q2 < 2; ++q2)
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (q4 * 32 + c < from || q4 * 32 + c >= to) sr[q4][c] = __float_as_uint(-INFINITY);
+            if (q2 * 32 + c < from || q2 * 32 + c >= to) sr[q2][c] = __float_as_uint(-INFINITY);
       }
       float mx = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < SUBS; ++b) {
+      for (int b = 0; b < 4; ++b) {
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 16; c += 4) {
@@ -504,8 +523,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           m0 = fmax3(m0, __uint_as_float(v[0]), __uint_as_float(v[1]));
           m1 = fmax3(m1, __uint_as_float(v[2]), __uint_as_float(v[3]));
         }
-        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(b), offset(b)));
+        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), f[b], e[b]));
       }
+      // the other half of the row: both threads go on with the same maximum
+      // (and P may now take the place of scores that the other thread has read)
+      my_max[(i & 1) * 128] = mx;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&max_full[w * 4 + quad]);
+      ok = __all_sync(~0u, mbar_wait(&max_full[w * 4 + quad], i & 1, wc));
+      if (!ok) break;
+      tc_fence_after();
+      mx = fmaxf(mx, other_max[(i & 1) * 128]);
       bool need = false;
       float alpha = 1.f;
       if (i == 0) {
@@ -518,31 +547,30 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - P_SHIFT;
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
+      for (int q2 = 0; q2 < 2; ++q2) {
         uint32_t pk[16];
 #pragma unroll
         for (int b2 = 0; b2 < 2; ++b2) {
-          const int b = q4 * 2 + b2;
-          const float f = factor(b), e = offset(b) - ref;
-          const float2 ff = make_float2(f, f), ee = make_float2(e, e);
+          const int b = q2 * 2 + b2;
+          const float2 ff = make_float2(f[b], f[b]), ee = make_float2(e[b] - ref, e[b] - ref);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint32_t* v = &sr[q4][b2 * 16 + 2 * c];
+            const uint32_t* v = &sr[q2][b2 * 16 + 2 * c];
             const float2 x = ffma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), ff, ee);
             const float2 pr = make_float2(ex2(x.x), ex2(x.y));
             sum = fadd2(sum, pr);
             pk[b2 * 8 + c] = pack_f16(pr.x, pr.y);
           }
-          l_sum = fmaf(sum.x + sum.y, sc.inv[b], l_sum);
+          l_sum = fmaf(sum.x + sum.y, inv[b], l_sum);
         }
-        tmem_st16(tS + q4 * 16, pk);
+        tmem_st16(tS + half * 32 + q2 * 16, pk);
       }
       if (__any_sync(~0u, need)) {
         // O of this group is quiescent: the commit that signalled this S also
         // covers the previous P V into it, and the next one waits for p_full.
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c0, o);
           tmem_wait_ld();
@@ -560,56 +588,79 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (ok && !*abort_flag) ok = mbar_wait(o_final, 0, wc);
     ok = __all_sync(~0u, ok);
     tc_fence_after();
-    if constexpr (!TWO) {
-      xch[w * 128 + row] = make_float2(m_ref, l_sum);
-      named_bar_sync(1, 256);
-    }
+    named_bar_sync(1, SOFTMAX);  // the maxima's slots are read
+    xch[(w * 2 + half) * 128 + row] = make_float2(m_ref, l_sum);
+    named_bar_sync(1, SOFTMAX);
     if (ok && !*abort_flag) {
-      // TWO: the group's O is its tile's; else the two groups' halves of the keys are joined, half the channels each
-      float m = m_ref, l = l_sum, a0 = 1.f, a1 = 0.f;
+      // the two threads of a row have one reference and half the sum each; without TWO the groups' halves of the
+      // keys are joined too.  Each thread writes SPAN channels.
+      float m = m_ref, l = l_sum + xch[(w * 2 + 1 - half) * 128 + row].y, a0 = 1.f, a1 = 0.f;
       bool both = false;
       if constexpr (!TWO) {
-        const float2 other = xch[(1 - w) * 128 + row];
-        m = fmaxf(m_ref, other.x);
+        const float2 x0 = xch[(2 - 2 * w) * 128 + row];
+        const float other_l = x0.y + xch[(3 - 2 * w) * 128 + row].y;
+        m = fmaxf(m_ref, x0.x);
         const float m0 = m == -INFINITY ? 0.f : m;
-        const float a_self = ex2(m_ref - m0), a_other = ex2(other.x - m0);
-        l = l_sum * a_self + other.y * a_other;  // a group without blocks has l = 0 and m = -inf
+        const float a_self = ex2(m_ref - m0), a_other = ex2(x0.x - m0);
+        l = l * a_self + other_l * a_other;  // a group without blocks has l = 0 and m = -inf
         a0 = w == 0 ? a_self : a_other;
         a1 = w == 0 ? a_other : a_self;
         both = nblk >= 2;
       }
+      l += poison;
       const float norm = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
       a0 *= norm;
       a1 *= norm;
-      const uint32_t t0 = TWO ? tO : tmem + lane_addr + 256u, t1 = tmem + lane_addr + 384u;
-      const size_t pr = ((size_t)shared * splits + split) * ROWS + brow;
-      constexpr int SPAN = TWO ? D : D / 2;
+      constexpr int SPAN = TWO ? D / 2 : D / 4;
+      const int col0 = (TWO ? half : w * 2 + half) * SPAN;
+      const uint32_t t0 = (TWO ? tO : tmem + lane_addr + 256u) + col0, t1 = tmem + lane_addr + 384u + col0;
+      float o[SPAN];
 #pragma unroll
-      for (int c = 0; c < SPAN; c += 32) {
-        const int c0 = (TWO ? 0 : w * SPAN) + c;
-        uint32_t x0[32], x1[32];
-        tmem_ld32(t0 + c0, x0);
-        if (!TWO && both) tmem_ld32(t1 + c0, x1);
+      for (int c = 0; c < SPAN; c += 16) {
+        uint32_t x1[16];
+        tmem_ld16(t0 + c, reinterpret_cast<uint32_t*>(o) + c);
+        if (!TWO && both) tmem_ld16(t1 + c, x1);
         tmem_wait_ld();
-        float* o = reinterpret_cast<float*>(x0);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = o[e] * a0 + (!TWO && both ? __uint_as_float(x1[e]) * a1 : 0.f);
-        if (real && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * D + c0);
+        for (int e = 0; e < 16; ++e) o[c + e] = o[c + e] * a0 + (!TWO && both ? __uint_as_float(x1[e]) * a1 : 0.f);
+      }
+      // through shared memory (every tile in it is done with), so that a warp stores whole runs of a row
+      uint8_t* stage = smem + warp * 32 * SPAN * 4;
+      const size_t pr = ((size_t)shared * splits + split) * ROWS + (TWO ? w * BM : 0) + quad * 32;
+      if (whole) {
+        constexpr int NCH = SPAN / 8, SH = NCH >= 8 ? 0 : NCH == 4 ? 1 : 2;
 #pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4)
-            dst[v4] = make_uint4(pack_bf16(o[8 * v4 + 0], o[8 * v4 + 1]), pack_bf16(o[8 * v4 + 2], o[8 * v4 + 3]),
-                                 pack_bf16(o[8 * v4 + 4], o[8 * v4 + 5]), pack_bf16(o[8 * v4 + 6], o[8 * v4 + 7]));
-        } else if (real) {
-          float4* dst = reinterpret_cast<float4*>(pp.part + pr * D + c0);
+        for (int c = 0; c < NCH; ++c)
+          *(uint4*)(stage + lane * SPAN * 2 + ((c ^ ((lane >> SH) & (NCH - 1))) << 4)) =
+              make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
+                         pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+        __syncwarp();
+        const int c = lane % NCH;
 #pragma unroll
-          for (int v4 = 0; v4 < 8; ++v4)
-            dst[v4] = make_float4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+        for (int i = 0; i < NCH; ++i) {
+          const int r = i * (32 / NCH) + lane / NCH;
+          const size_t to = __shfl_sync(~0u, out_row, r);
+          const uint4 v = *(const uint4*)(stage + r * SPAN * 2 + ((c ^ ((r >> SH) & (NCH - 1))) << 4));
+          if ((TWO ? w * BM : 0) + quad * 32 + r < rows) *(uint4*)(p.o + to * D + col0 + c * 8) = v;
+        }
+      } else {
+        constexpr int NCH = SPAN / 4, SH = NCH >= 8 ? 0 : 1, MASK = NCH >= 8 ? 7 : NCH - 1;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          *(float4*)(stage + lane * SPAN * 4 + ((c ^ ((lane >> SH) & MASK)) << 4)) =
+              make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        __syncwarp();
+        const int c = lane % NCH;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const int r = i * (32 / NCH) + lane / NCH;
+          const float4 v = *(const float4*)(stage + r * SPAN * 4 + ((c ^ ((r >> SH) & MASK)) << 4));
+          *(float4*)(pp.part + (pr + r) * D + col0 + c * 4) = v;
         }
       }
-      if ((TWO || w == 0) && real) {
+      if (half == 0 && (TWO || w == 0) && real) {
         if (!whole)
-          pp.part_ml[pr] = make_float2(m, l);
+          pp.part_ml[pr + lane] = make_float2(m, l);
         else if (p.lse)
           p.lse[out_row] = (m - P_SHIFT + __log2f(l)) * 0.69314718055994531f;
       }
