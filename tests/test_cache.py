@@ -226,7 +226,10 @@ def test_refusals(V):
         ("table_width", 0, INV), ("frame_tokens", -1, INV), ("window_frames", -1, INV), ("window_frames", 2, INV),
         ("head_dim", 96, UNS), ("head_dim", 256, UNS), ("page_tokens", 8, UNS), ("page_tokens", 48, UNS),
         ("page_tokens", 256, UNS), ("q_heads", 65536, UNS), ("streams", 65536, UNS), ("pages", 1 << 27, UNS),
-        ("pages", 1 << 60, UNS), ("table_width", 1 << 27, UNS)]]
+        ("pages", 1 << 60, UNS), ("table_width", 1 << 27, UNS), ("table_width", (1 << 27) - 8, UNS)]]
+    cases += [(lambda: _plan(V, _geom(V, streams=65535, kv_heads=65535, q_heads=65535)), UNS),
+              (lambda: _plan(V, _geom(V, pages=1 << 26, kv_heads=64, q_heads=64)), UNS),
+              (lambda: V.vattn_cache_workspace_size(_geom(V, q_heads=64, kv_heads=1), 1 << 28, 1 << 28), UNS)]
     cases += [(lambda k=k: _plan(V, g, **{k: 0}), INV) for k in
               ("new", "lens", "table", "free", "n_free", "lens_out", "n_free_out", "starts", "slots", "result")]
     cases += [

@@ -377,6 +377,12 @@ def test_single_tokens(d, kv_heads, group, pt, steps):
     _check(d=d, kv_heads=kv_heads, group=group, pt=pt, steps=steps, seed=pt + group)
 
 
+def test_many_streams():
+    """More streams than a thread block has threads, most of them short, some idle."""
+    steps = [(i * 53 % 90, 1 if i % 7 and i * 53 % 90 else 0) for i in range(700)] + [(3000, 1), (1, 1), (700, 1)]
+    _check(d=64, kv_heads=2, group=1, pt=16, steps=steps, seed=30)
+
+
 FEW = [
     ([(9, 5)], 1, 0), ([(200, 8), (31, 1), (8, 8), (130, 3)], 1, 0), ([(257, 4), (63, 7)], 0, 0),
     ([(100, 6), (333, 8)], 4, 2), ([(3, 8), (0, 3), (2, 2)], 1, 0), ([(500, 5), (90, 5)], 7, 1), ([(300, 3)], 1, 40),

@@ -63,8 +63,10 @@ int build_geom(const vattn_cache_geom* in, cache::Geom* g) {
   if (in->pages >= (1ll << 31) / pt) return fail(VATTN_ERR_UNSUPPORTED, "pages * page_tokens must be < 2^31");
   if (in->pages * in->kv_heads >= (1ll << 31))
     return fail(VATTN_ERR_UNSUPPORTED, "pages * kv_heads must be < 2^31");
-  if ((long long)in->table_width * pt >= (1ll << 31))
-    return fail(VATTN_ERR_UNSUPPORTED, "table_width * page_tokens must be < 2^31");
+  if (in->streams * in->kv_heads >= (1ll << 31))
+    return fail(VATTN_ERR_UNSUPPORTED, "streams * kv_heads must be < 2^31");
+  if ((long long)in->table_width * pt >= (1ll << 31) - 256)
+    return fail(VATTN_ERR_UNSUPPORTED, "table_width * page_tokens must be < 2^31 - 256");
   g->streams = (int)in->streams;
   g->q_heads = (int)in->q_heads;
   g->kv_heads = (int)in->kv_heads;
@@ -180,7 +182,9 @@ int vattn_cache_workspace_size(const vattn_cache_geom* geom, int64_t n_tokens, i
   if ((r = check_tokens(n_tokens))) return r;
   if (max_new < 0) return fail(VATTN_ERR_INVALID_ARG, "max_new must be >= 0");
   if (!bytes) return fail(VATTN_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = fwd_workspace(g, max_new < n_tokens ? max_new : n_tokens);
+  if (max_new > n_tokens) max_new = n_tokens;
+  if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
+  *bytes = fwd_workspace(g, max_new);
   return ok();
 }
 
@@ -195,6 +199,7 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   if (max_new < 0) return fail(VATTN_ERR_INVALID_ARG, "max_new must be >= 0");
   if (!(scale > 0.f) || std::isinf(scale)) return fail(VATTN_ERR_INVALID_ARG, "scale must be positive and finite");
   if (max_new > n_tokens) max_new = n_tokens;
+  if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
   if (g.streams == 0 || n_tokens == 0 || max_new == 0) return ok();
   if ((r = check_stride("q_stride", q_stride, g.q_heads, g.d))) return r;
   REQUIRE_PTR(q);

@@ -44,7 +44,17 @@ constexpr float RESCALE = 8.0f;
 // Two partial results a thread block: of the (stream, head) that began before
 // its tiles (slot 0) and of the one that goes on after them (slot 1).
 constexpr int SLOTS = GRID * 2;
-inline size_t workspace_bytes(int d) { return (size_t)SLOTS * ROWS * (d + 2) * sizeof(float); }
+// What a thread block leaves to be joined with the partial results of those
+// after it, in its second slot: `blocks` of them share it (0: nothing).
+struct Shared {
+  int row0, head, rows, blocks;  // first token, kv head, query rows
+};
+inline size_t workspace_bytes(int d) {
+  return (size_t)SLOTS * ROWS * (d + 2) * sizeof(float) + GRID * sizeof(Shared);
+}
+__device__ __forceinline__ Shared* shared_of(void* ws, int d) {
+  return (Shared*)((float*)ws + (size_t)SLOTS * ROWS * (d + 2));
+}
 __device__ __forceinline__ float* slot_o(void* ws, int d, int slot) { return (float*)ws + (size_t)slot * ROWS * d; }
 __device__ __forceinline__ float2* slot_ml(void* ws, int d, int slot) {
   return (float2*)((float*)ws + (size_t)SLOTS * ROWS * d) + (size_t)slot * ROWS;
@@ -236,7 +246,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
   const Shares shares(pl.total);
   long long at = shares.first(blockIdx.x);
   const long long stop = shares.first(blockIdx.x + 1);
-  if (at >= stop) return;
+  Shared left = {0, 0, 0, 0};
+  if (at >= stop) {
+    if (threadIdx.x == 0) shared_of(ws, D)[blockIdx.x] = left;
+    return;
+  }
   int s = pl.stream;
   long long first = pl.first;  // first tile of stream s
   StreamTiles sp = stream_tiles(p, s);
@@ -250,8 +264,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
     const int h = in_stream < (1ll << 31) ? (uint32_t)in_stream / (uint32_t)sp.tiles : (int)(in_stream / sp.tiles);
     const int k0 = (int)(in_stream - (long long)h * sp.tiles);
     const int k1 = (int)min((long long)sp.tiles, k0 + (stop - at));
-    at += k1 - k0;
     const int rows = sp.st.n * g.group;
+    if (k0 == 0 && k1 < sp.tiles)
+      left = {sp.st.row0, h, rows, shares.owner(at + sp.tiles - 1) - (int)blockIdx.x + 1};
+    at += k1 - k0;
     const int min_lo = sp.lo, max_hi = sp.end;
 
     // steps of this warp: keys sp.base + (k * WARPS + warp) * STEP, k in [k0, k1)
@@ -579,47 +595,24 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
     }
     __syncthreads();
   }
+  if (threadIdx.x == 0) shared_of(ws, D)[blockIdx.x] = left;
 }
 
-// Joins the partial results of each row that several thread blocks share: their
-// weights first, then groups of d / 4 threads take every so-manieth one, with
-// several loads in flight.
+// Joins the partial results of a row of a (stream, head) that several thread
+// blocks share, the first of them blockIdx.x: their weights first, then groups
+// of d / 4 threads take every so-manieth one, with several loads in flight.
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const FwdParams p, void* ws) {
   constexpr int LANES = D / 4, GROUPS = 128 / LANES;
-  __shared__ long long part[8];
   __shared__ float weight[GRID];
   __shared__ float red[4];
   __shared__ float4 accs[128];
   const Geom& g = p.g;
-  const int t = threadIdx.x;
-  const int s = blockIdx.x / g.kv_heads, h = blockIdx.x % g.kv_heads, r = blockIdx.y;
-  // first tile of stream s, and all tiles
-  long long mine = 0, all = 0;
-  for (int i = t; i < g.streams; i += 128) {
-    const int n = stream_tiles(p, i).tiles;
-    all += n;
-    if (i < s) mine += n;
-  }
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += __shfl_xor_sync(~0u, mine, o);
-    all += __shfl_xor_sync(~0u, all, o);
-  }
-  if ((t & 31) == 0) {
-    part[t >> 5] = mine;
-    part[4 + (t >> 5)] = all;
-  }
-  __syncthreads();
-  const long long before = (part[0] + part[1] + part[2] + part[3]) * g.kv_heads;
-  const long long total = (part[4] + part[5] + part[6] + part[7]) * g.kv_heads;
-  const StreamTiles sp = stream_tiles(p, s);
+  const int t = threadIdx.x, r = blockIdx.y, c0 = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (r >= sp.st.n * g.group) return;
-  const long long t0 = before + (long long)h * sp.tiles;
-  const Shares shares(total);
-  const int c0 = shares.owner(t0), c1 = shares.owner(t0 + sp.tiles - 1);
-  if (c0 == c1) return;
-  const int n = c1 - c0 + 1;
+  const int4 left = __ldcg((const int4*)(shared_of(ws, D) + c0));
+  const int row0 = left.x, h = left.y, n = left.w;
+  if (n == 0 || r >= left.z) return;
   // partial result i: block c0 keeps it in its second slot, the others in their first
   auto slot_of = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
   auto block_reduce = [&](float v, bool sum) {
@@ -673,7 +666,7 @@ __global__ void __launch_bounds__(128) join_kernel(const FwdParams p, void* ws) 
     acc.w += v.w;
   }
   const int tok = r / g.group;
-  const size_t at_o = (size_t)(sp.st.row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
+  const size_t at_o = (size_t)(row0 + tok) * g.q_heads + h * g.group + (r - tok * g.group);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *(uint2*)(p.o + at_o * D + c) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   if (c == 0 && p.lse) p.lse[at_o] = (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
@@ -689,7 +682,7 @@ cudaError_t launch(const FwdParams& p, void* ws, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.g.streams * p.g.kv_heads), (unsigned)(p.max_new * p.g.group));
+  cfg.gridDim = dim3(GRID, (unsigned)(p.max_new * p.g.group));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr;

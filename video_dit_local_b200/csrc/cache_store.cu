@@ -409,7 +409,7 @@ cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, 
   const int span = (long long)a.n_tokens / 16 * g.kv_heads >= 148 * 16 ? 16 : 1;
   const long long warps = (long long)((a.n_tokens + span - 1) / span) * g.kv_heads;
   const long long blocks = (warps + APPEND_WARPS - 1) / APPEND_WARPS;
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (warps >= (1ll << 31)) return cudaErrorInvalidValue;
   if (g.d == 128)
     append_kernel<128><<<(int)blocks, APPEND_WARPS * 32, 0, st>>>(g, a, span);
   else
