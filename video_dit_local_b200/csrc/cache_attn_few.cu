@@ -273,20 +273,22 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
     // steps of this warp: keys sp.base + (k * WARPS + warp) * STEP, k in [k0, k1)
     const int* table = p.table + (long long)s * g.width;
     auto step_key = [&](int k) { return sp.base + (k * WARPS + warp) * STEP; };
-    // Pages of the two 16-key halves of the next step to be loaded, as read from the table (-1: none of its keys
-    // is to be read).  They are looked at only when that step is loaded, a step later, so that no warp waits here.
-    int raw0 = -1, raw1 = -1;
-    auto fetch_pages = [&](int k) {
-      if (k >= k1) return;
-      const int a = step_key(k), b = a + SCALE_TOKENS;
-      raw0 = a < max_hi && b > min_lo ? __ldg(table + (a >> g.page_shift)) : -1;
-      raw1 = b < max_hi && b + SCALE_TOKENS > min_lo ? __ldg(table + (b >> g.page_shift)) : -1;
+    // Pages of a step's two 16-key halves as read from the table (-1: none of its keys is to be read).  They are
+    // looked at only when the step is loaded, later on, so that no warp waits here.
+    auto pages_of = [&](int k) {
+      int2 r = make_int2(-1, -1);
+      if (k < k1) {
+        const int a = step_key(k), b = a + SCALE_TOKENS;
+        if (a < max_hi && b > min_lo) r.x = __ldg(table + (a >> g.page_shift));
+        if (b < max_hi && b + SCALE_TOKENS > min_lo) r.y = __ldg(table + (b >> g.page_shift));
+      }
+      return r;
     };
-    auto load = [&](int k) {
+    auto load = [&](int k, const int2& raw) {
       if (k < k1) {
         const int key0 = step_key(k);
         const uint32_t dst = ring + ((k - k0) % R::STAGES) * R::STAGE;
-        const int pg0 = raw0 < g.pages ? raw0 : -1, pg1 = raw1 < g.pages ? raw1 : -1;
+        const int pg0 = raw.x < g.pages ? raw.x : -1, pg1 = raw.y < g.pages ? raw.y : -1;
         if ((pg0 < 0 && key0 < max_hi && key0 + SCALE_TOKENS > min_lo) ||
             (pg1 < 0 && key0 + SCALE_TOKENS < max_hi && key0 + STEP > min_lo))
           report_error(p.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
@@ -343,11 +345,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
       }
     }
     // the first keys are on their way before the rows are needed
-    fetch_pages(k0);
+    int2 next;
+    {
+      int2 raw[R::STAGES];
 #pragma unroll
-    for (int i = 0; i < R::STAGES - 1; ++i) {
-      load(k0 + i);
-      fetch_pages(k0 + i + 1);
+      for (int i = 0; i < R::STAGES; ++i) raw[i] = pages_of(k0 + i);
+#pragma unroll
+      for (int i = 0; i < R::STAGES; ++i) load(k0 + i, raw[i]);
+      next = pages_of(k0 + R::STAGES);
     }
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -390,8 +395,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) few_kernel(const FwdPara
     }
 
     for (int k = k0; k < k1; ++k) {
-      load(k + R::STAGES - 1);
-      fetch_pages(k + R::STAGES);
+      if (k > k0) {  // into the stage that the last step left
+        load(k + R::STAGES - 1, next);
+        next = pages_of(k + R::STAGES);
+      }
       cp_wait<R::STAGES - 1>();
       __syncwarp();
       const uint32_t st = ring + ((k - k0) % R::STAGES) * R::STAGE;
