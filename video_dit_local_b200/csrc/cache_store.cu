@@ -241,7 +241,10 @@ __global__ void __launch_bounds__(256) slots_kernel(const Geom g, const CachePla
 // Append.  A warp takes one 16-token block of one kv head (K and V): its new
 // rows are read once into registers (all loads in flight together), the block's
 // absmax gives the scale exponent, and the bytes leave in whole cache rows.
-// Bound by HBM: 4 d bytes in, 2 d bytes out per token and kv head.
+// Bound by HBM: 4 d bytes in, 2 d bytes out per token and kv head (two 1080p
+// frames, 24 heads of 128, from a fused projection: 51 us, 6.2 TB/s).  That
+// leaves about 600 instructions a block: a block of sixteen finite new tokens,
+// which is what a frame is made of, takes a path without predicates.
 // ---------------------------------------------------------------------------
 
 // Smallest e >= E_MIN with the bf16 magnitude `bits` (finite) <= 448 * 2^e:
@@ -254,8 +257,9 @@ __device__ __forceinline__ float pow2(int e) {  // e in [-126, 127]
   return __int_as_float((e + 127) << 23);
 }
 
-// Warps of a thread block: small blocks fit the registers better (66 us for two
-// 1080p frames; 85 with eight warps, 8 us more for ragged chunks with one).
+// Warps of a thread block: small blocks fit the registers better (eight
+// warps took 29% longer for two 1080p frames, one warp twice as long for ragged
+// chunks).
 constexpr int APPEND_WARPS = 4;
 
 template <int D>
@@ -291,41 +295,51 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const Geom g,
     const long long sidx = row >> 4;
     // rows are counted from the block's first: row r is new token i + r - held
     uint4 kx[NL], vx[NL];
-    const __nv_bfloat16* kp = (const __nv_bfloat16*)a.k + h * D + c * 8;
-    const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + h * D + c * 8;
+    const __nv_bfloat16* kp = (const __nv_bfloat16*)a.k + (i + r0 - held) * a.k_stride + h * D + c * 8;
+    const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + (i + r0 - held) * a.v_stride + h * D + c * 8;
+    const bool full = n == 16;  // then held = 0
+    uint32_t km2 = 0, vm2 = 0;  // largest magnitudes, two packed
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
       const int r = l * RPL + r0 - held;
-      const bool in = r >= 0 && r < n;
-      kx[l] = in ? __ldg((const uint4*)(kp + (i + r) * a.k_stride)) : make_uint4(0, 0, 0, 0);
-      vx[l] = in ? __ldg((const uint4*)(vp + (i + r) * a.v_stride)) : make_uint4(0, 0, 0, 0);
+      const bool in = full || (r >= 0 && r < n);
+      kx[l] = in ? __ldg((const uint4*)(kp + l * RPL * a.k_stride)) : make_uint4(0, 0, 0, 0);
+      vx[l] = in ? __ldg((const uint4*)(vp + l * RPL * a.v_stride)) : make_uint4(0, 0, 0, 0);
     }
-    uint32_t km = 0, vm = 0, poison = 0;
+    auto magnitude = [](const uint4& x) {
+      return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    };
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
-      auto row_max = [](const uint4& x) {
-        uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                              __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-        return max(m & 0xffffu, m >> 16);
-      };
-      uint32_t a_k = row_max(kx[l]), a_v = row_max(vx[l]);
-      uint32_t both = (a_k << 16) | a_v;
+      km2 = __vmaxu2(km2, magnitude(kx[l]));
+      vm2 = __vmaxu2(vm2, magnitude(vx[l]));
+    }
+    uint32_t both = max(km2 & 0xffffu, km2 >> 16) << 16 | max(vm2 & 0xffffu, vm2 >> 16);
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(~0u, both, o));
-      a_k = both >> 16;
-      a_v = both & 0xffffu;
-      if (a_k >= 0x7f80u || a_v >= 0x7f80u) {  // a NaN or an infinity: the token gives no magnitude
-        poison |= 1u << l;
-      } else {
-        km = max(km, a_k);
-        vm = max(vm, a_v);
+    for (int o = 16; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(~0u, both, o));
+    uint32_t km = both >> 16, vm = both & 0xffffu, poison = 0;
+    if (km >= 0x7f80u || vm >= 0x7f80u) {  // a NaN or an infinity somewhere: its token gives no magnitude
+      km = vm = 0;
+#pragma unroll
+      for (int l = 0; l < NL; ++l) {
+        const uint32_t k2 = magnitude(kx[l]), v2 = magnitude(vx[l]);
+        uint32_t row = max(k2 & 0xffffu, k2 >> 16) << 16 | max(v2 & 0xffffu, v2 >> 16);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) row = __vmaxu2(row, __shfl_xor_sync(~0u, row, o));
+        if ((row >> 16) >= 0x7f80u || (row & 0xffffu) >= 0x7f80u) {
+          poison |= 1u << l;
+        } else {
+          km = max(km, row >> 16);
+          vm = max(vm, row & 0xffffu);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o >= LPR; o >>= 1) {
+        km = max(km, __shfl_xor_sync(~0u, km, o));
+        vm = max(vm, __shfl_xor_sync(~0u, vm, o));
       }
     }
-#pragma unroll
-    for (int o = 16; o >= LPR; o >>= 1) {
-      km = max(km, __shfl_xor_sync(~0u, km, o));
-      vm = max(vm, __shfl_xor_sync(~0u, vm, o));
-    }
+    const bool clean = full && __all_sync(~0u, poison == 0);
     int ke = scale_exponent(km), ve = scale_exponent(vm);
     int ke_old = ke, ve_old = ve;
     if (held > 0) {
@@ -338,6 +352,24 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const Geom g,
     if (lane == 0) {
       a.ks[sidx] = pow2(ke);
       a.vs[sidx] = pow2(ve);
+    }
+    auto quantise = [](const uint4& x, float f) {
+      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+      uint32_t out[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) out[u] = pack_e4m3x2(bf16lo(in[u]) * f, bf16hi(in[u]) * f);
+      return make_uint2(out[0] | (out[1] << 16), out[2] | (out[3] << 16));
+    };
+    if (clean) {  // sixteen new tokens, nothing to keep or to mark
+      uint2* kd = (uint2*)((uint8_t*)a.kc + (row + r0) * D + c * 8);
+      uint2* vd = (uint2*)((uint8_t*)a.vc + (row + r0) * D + c * 8);
+      const float kf = pow2(-ke), vf = pow2(-ve);
+#pragma unroll
+      for (int l = 0; l < NL; ++l) {
+        kd[l * RPL * D / 8] = quantise(kx[l], kf);
+        vd[l * RPL * D / 8] = quantise(vx[l], vf);
+      }
+      continue;
     }
     auto store = [&](const uint4& x, uint8_t* base, int r, int e, int e_old, bool nan, bool zero) {
       uint2* dst = (uint2*)(base + (row + r) * D + c * 8);
@@ -361,12 +393,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const Geom g,
       } else if (nan) {
         *dst = make_uint2(0x01010101u * E4M3_NAN, 0x01010101u * E4M3_NAN);
       } else {
-        const float f = pow2(-e);
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t out[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) out[u] = pack_e4m3x2(bf16lo(in[u]) * f, bf16hi(in[u]) * f);
-        *dst = make_uint2(out[0] | (out[1] << 16), out[2] | (out[3] << 16));
+        *dst = quantise(x, pow2(-e));
       }
     };
 #pragma unroll
