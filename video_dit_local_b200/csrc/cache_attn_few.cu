@@ -8,7 +8,8 @@
 //    three thread blocks of four warps keep about 100 KB in flight on an SM,
 //    twice what the memory latency needs at full rate;
 //  - a fixed grid shares all streams' 128-key tiles evenly, whatever their
-//    lengths: every thread block takes an equal run of the tiles, which are laid out stream by stream and head by head.  A (stream, head) that
+//    lengths: thread blocks take equal runs of the tiles, which are laid out
+//    stream by stream and head by head.  A (stream, head) that
 //    spans several thread blocks leaves partial results that a second kernel
 //    joins in a fixed order; it is launched early (programmatic dependent
 //    launch) so that only its joins are exposed.
@@ -141,20 +142,32 @@ __device__ __forceinline__ uint32_t v_at(int row, int chunk) {
                   : (row ^ ((row >> 1) & 1)) * 64 + ((chunk ^ (((row >> 2) & 1) << 1)) << 4);
 }
 
-// `total` tiles shared evenly: each of the first `extra` thread blocks takes
-// per + 1 of them, each of the others `per` (blocks past total take none).
+// `total` tiles shared evenly: the first `extra` thread blocks take per + 1 of
+// them, the others `per` (and those past the last tile none).  With few tiles a
+// block no more blocks than needed take part: 792 tiles (one token over 4101
+// keys, 24 heads) go to 396 blocks of two, not to 348 of two and 96 of one,
+// which end at the same time but leave more to join (13.6 against 14.1 us); with
+// many, the blocks of an SM share its bandwidth, and all of them are wanted
+// (54 against 59 us for a few tokens in 16 streams).
 struct Shares {
-  long long per, extra;
-  __device__ __forceinline__ explicit Shares(long long total) {
-    per = total < (1ll << 31) ? (uint32_t)total / GRID : total / GRID;
-    extra = total - per * GRID;
+  long long per, extra, total;
+  __device__ __forceinline__ explicit Shares(long long t) : total(t) {
+    if (t < 4 * GRID) {
+      per = ((uint32_t)t + GRID - 1) / GRID;
+      extra = 0;
+    } else {
+      per = t < (1ll << 31) ? (uint32_t)t / GRID : t / GRID;
+      extra = t - per * GRID;
+    }
   }
-  __device__ __forceinline__ long long first(int block) const { return block * per + min((long long)block, extra); }
+  __device__ __forceinline__ long long first(int block) const {
+    return min(block * per + min((long long)block, extra), total);
+  }
   __device__ __forceinline__ int owner(long long tile) const {
     const long long wide = extra * (per + 1);  // tiles of the blocks that take one more
-    if (tile < wide) return per < (1ll << 30) && wide < (1ll << 31) ? (uint32_t)tile / (uint32_t)(per + 1) : tile / (per + 1);
-    const long long r = tile - wide;
-    return (int)extra + (r < (1ll << 31) && per < (1ll << 31) ? (uint32_t)r / (uint32_t)per : r / per);
+    const bool small = total < (1ll << 31);
+    if (tile < wide) return small ? (uint32_t)tile / (uint32_t)(per + 1) : (int)(tile / (per + 1));
+    return (int)extra + (small ? (uint32_t)(tile - wide) / (uint32_t)per : (int)((tile - wide) / per));
   }
 };
 
