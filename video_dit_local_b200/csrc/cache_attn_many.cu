@@ -62,7 +62,11 @@ struct alignas(16) Scales {
 template <int D, bool TWO>
 struct Smem {
   static constexpr int TILES = TWO ? 2 : 1;     // tiles of query rows
-  static constexpr int NK = TWO ? 2 : 3;        // ring stages of K and of V's bytes
+  static constexpr int NK = TWO && D == 128 ? 2 : 3;  // ring stages of K and of V's bytes
+  // S accumulators (TMEM columns 128 b ..) and O accumulators (from column 128 NB, d columns a group).  At d = 64 a
+  // third S fits: Q K^T then runs ahead of the softmax (see the MMA warp).
+  static constexpr int NB = D == 64 ? 3 : 2;
+  static constexpr uint32_t O = 128 * NB;
   static constexpr int QK = 128 * D;            // 128 rows of bytes
   static constexpr int V = 128 * D * 2;         // 128 rows of f16
   static constexpr int OFF_Q = 0;               // hi and lo of each tile
@@ -72,7 +76,7 @@ struct Smem {
   static constexpr int OFF_SC = OFF_V + NV * V;              // NS x Scales
   static constexpr int OFF_XCH = OFF_SC + NS * (int)sizeof(Scales);
   static constexpr int OFF_BAR = OFF_XCH + 4 * 128 * 8;      // [group][half][row] pairs of floats
-  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 1 + NS + 8;
+  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 * NB + 2 + 1 + NS + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int TOTAL = OFF_MISC + 16;
   static constexpr int ALLOC = TOTAL + 1024;
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const Params pp) {
   using L = Smem<D, TWO>;
-  constexpr int NK = L::NK;
+  constexpr int NK = L::NK, NB = L::NB;
   constexpr int ROWS = L::TILES * BM;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -198,9 +202,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* v8_empty = k_empty + NK; // V's bytes of a stage are converted
   uint64_t* v_full = v8_empty + NK;
   uint64_t* v_empty = v_full + NV;
-  uint64_t* s_full = v_empty + NV;   // a group's next S is in TMEM
-  uint64_t* p_full = s_full + 2;     // ... and its P
-  uint64_t* o_final = p_full + 2;
+  uint64_t* s_full = v_empty + NV;   // S of an accumulator is in TMEM
+  uint64_t* p_full = s_full + NB;    // ... and its P
+  uint64_t* pv_done = p_full + NB;   // a group's last P V is done (three S accumulators)
+  uint64_t* o_final = pv_done + 2;
   uint64_t* sc_full = o_final + 1;
   uint64_t* max_full = sc_full + NS;  // [group][quad]: both halves of the rows' maxima are there
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -223,10 +228,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&v_full[i], V_WARPS);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&pv_done[i], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&max_full[i], 2);
     mbar_init(o_final, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&sc_full[i], 1);
@@ -357,9 +363,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t k_base = smem_u32(smem + L::OFF_K);
       const uint32_t v_base = smem_u32(smem + L::OFF_V);
       bool ok = mbar_wait(q_full, 0, wc);
-      // S of group w = Q (of its tile) K_j^T
-      auto issue_qk = [&](int j, int w, bool last_of_k) -> bool {
-        const int sg = j % NK;
+      // Unit n: S and then O of group n & 1, with key block n / 2 (TWO) or n, in S accumulator n % NB.  Two
+      // accumulators: Q K^T of unit n + 2 follows P V of unit n, and the group waits for both.  Three: it follows P V
+      // of unit n - 1, so that the next S is there when the group has stored its P.
+      auto issue_qk = [&](int n) -> bool {
+        const int j = TWO ? n >> 1 : n, w = n & 1, sg = j % NK, b = n % NB;
         if (!mbar_wait(&kv_full[sg], (j / NK) & 1, wc)) return false;
         tc_fence_after();
         const uint32_t kb = k_base + sg * L::QK, qb = q_base + (TWO ? w : 0) * 2 * L::QK;
@@ -367,41 +375,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int part = 0; part < 2; ++part)  // hi, lo
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_ss_e4m3(tmem + (uint32_t)(w * 128), desc_bytes<D>(qb + part * L::QK + kk * 32),
+            mma_ss_e4m3(tmem + (uint32_t)(b * 128), desc_bytes<D>(qb + part * L::QK + kk * 32),
                         desc_bytes<D>(kb + kk * 32), idesc_e4m3_f32(BM, BN), part + kk > 0);
-        tc_commit(&s_full[w]);
-        if (last_of_k) tc_commit(&k_empty[sg]);
+        tc_commit(&s_full[b]);
+        if (!TWO || w == 1) tc_commit(&k_empty[sg]);
         return true;
       };
-      // O of group w += P V_j; i: the group's how-manieth block
-      auto issue_pv = [&](int j, int w, int i, bool last_of_v) -> bool {
-        const int sg = j % NV;
-        if (!mbar_wait(&p_full[w], i & 1, wc)) return false;
+      auto issue_pv = [&](int n) -> bool {
+        const int j = TWO ? n >> 1 : n, w = n & 1, sg = j % NV, b = n % NB;
+        if (!mbar_wait(&p_full[b], (n / NB) & 1, wc)) return false;
         if (!mbar_wait(&v_full[sg], (j / NV) & 1, wc)) return false;
         tc_fence_after();
         const uint32_t vb = v_base + sg * L::V;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tmem + 256 + (uint32_t)(w * 128), tmem + (uint32_t)(w * 128) + kk * 8,
-                 smem_desc_sw128(vb + kk * 2048, 128 * 128, 1024), idesc_f16_pv(D), (i > 0 || kk > 0) ? 1u : 0u);
-        if (last_of_v) tc_commit(&v_empty[sg]);
+          mma_ts(tmem + L::O + (uint32_t)(w * D), tmem + (uint32_t)(b * 128) + kk * 8,
+                 smem_desc_sw128(vb + kk * 2048, 128 * 128, 1024), idesc_f16_pv(D), (n >= 2 || kk > 0) ? 1u : 0u);
+        if (NB > 2) tc_commit(&pv_done[w]);
+        if (!TWO || w == 1) tc_commit(&v_empty[sg]);
         return true;
       };
-      if constexpr (TWO) {
-        ok = ok && issue_qk(0, 0, false) && issue_qk(0, 1, true);
-        for (int j = 0; ok && j < nblk; ++j) {
-          ok = issue_pv(j, 0, j, false);
-          if (ok && j + 1 < nblk) ok = issue_qk(j + 1, 0, false);
-          ok = ok && issue_pv(j, 1, j, true);
-          if (ok && j + 1 < nblk) ok = issue_qk(j + 1, 1, true);
-        }
-      } else {
-        ok = ok && issue_qk(0, 0, true);
-        if (ok && nblk > 1) ok = issue_qk(1, 1, true);
-        for (int j = 0; ok && j < nblk; ++j) {
-          ok = issue_pv(j, j & 1, j >> 1, true);
-          if (ok && j + 2 < nblk) ok = issue_qk(j + 2, j & 1, true);
-        }
+      const int units = TWO ? 2 * nblk : nblk;
+      for (int n = 0; ok && n < min(NB, units); ++n) ok = issue_qk(n);
+      for (int n = 0; ok && n < units; ++n) {
+        ok = issue_pv(n);
+        if (ok && n + NB < units) ok = issue_qk(n + NB);
       }
       tc_commit(o_final);
       // every MMA this thread issued must be finished before TMEM is freed
@@ -475,23 +473,32 @@ __global__ void __launch_bounds__(THREADS, 1)
       named_bar_sync(1, SOFTMAX);
     }
     const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_addr + (uint32_t)(w * 128);
-    const uint32_t tO = tmem + lane_addr + 256u + (uint32_t)(w * 128);
+    const uint32_t tO = tmem + lane_addr + L::O + (uint32_t)(w * D);
     float* my_max = (float*)xch + (w * 2 + half) * 256 + row;          // two slots, 128 floats apart
     const float* other_max = (float*)xch + (w * 2 + 1 - half) * 256 + row;
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
-    for (int i = 0;; ++i) {
+    int acc = w;            // S accumulator of the group's unit 2 i + w ...
+    uint32_t acc_phase = 0; // ... and the parity of its use
+    auto next_unit = [&] {
+      acc += 2;
+      if (acc >= NB) {
+        acc -= NB;
+        acc_phase ^= 1u;
+      }
+    };
+    for (int i = 0;; ++i, next_unit()) {
       const int j = TWO ? i : 2 * i + w;
       if (j >= nblk) break;
-      ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&s_full[w], i & 1, wc);
+      const uint32_t tS = tmem + lane_addr + (uint32_t)(acc * 128);
+      ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&s_full[acc], acc_phase, wc);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after();
       if (idle) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
+        if (lane == 0) mbar_arrive(&p_full[acc]);
         continue;
       }
       // this thread's 64 scores: keys 64 half .. of the block
@@ -568,7 +575,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (__any_sync(~0u, need)) {
         // O of this group is quiescent: the commit that signalled this S also
-        // covers the previous P V into it, and the next one waits for p_full.
+        // covers the previous P V into it (two accumulators; with three it is
+        // waited for), and the next one waits for p_full.
+        if (NB > 2 && i > 0) {
+          ok = __all_sync(~0u, mbar_wait(&pv_done[w], (i - 1) & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+        }
 #pragma unroll 1
         for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[w]);
+      if (lane == 0) mbar_arrive(&p_full[acc]);
     }
     // ---------------- epilogue ----------------
     if (ok && !*abort_flag) ok = mbar_wait(o_final, 0, wc);
@@ -613,7 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       a1 *= norm;
       constexpr int SPAN = TWO ? D / 2 : D / 4;
       const int col0 = (TWO ? half : w * 2 + half) * SPAN;
-      const uint32_t t0 = (TWO ? tO : tmem + lane_addr + 256u) + col0, t1 = tmem + lane_addr + 384u + col0;
+      const uint32_t t0 = (TWO ? tO : tmem + lane_addr + L::O) + col0, t1 = tmem + lane_addr + L::O + D + col0;
       float o[SPAN];
 #pragma unroll
       for (int c = 0; c < SPAN; c += 16) {
