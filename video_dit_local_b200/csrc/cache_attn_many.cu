@@ -7,11 +7,11 @@
 //   warps 0-7 and 8-15 two softmax groups, each with an S and an O accumulator
 //                      in TMEM; a row's 128 scores are shared by two threads,
 //                      64 each (720p frame over ten: 1.89 ms; 1.93 with one
-//                      thread a row and half as many warps).  TWO = true: a tile of rows each (256 rows a
-//                      thread block), on the same key blocks, so that one
-//                      conversion of V serves 256 rows; false (no stream has
-//                      more than 128 rows): one tile, alternate key blocks,
-//                      joined at the end;
+//                      thread a row and half as many warps).  TWO = true: a
+//                      tile of rows each (256 rows a thread block), on the same
+//                      key blocks, so that one conversion of V serves 256
+//                      rows; false (no stream has more than 128 rows): one
+//                      tile, alternate key blocks, joined at the end;
 //   warps 16, 17       convert V, e4m3 -> f16, from one swizzled tile into the
 //                      other that P V reads;
 //   warp 18            K and V pages by TMA, and the blocks' scales;
@@ -87,30 +87,21 @@ struct Params {
   int q_tiles;   // tiles of rows (of all of a thread block's) that a stream can have
   int whole;     // items (a tile of rows, kv head and stream) with a thread block each
   int splits;    // thread blocks that share the keys of each of the other items
-  int tile_slow; // order of the items: streams, kv heads, tiles (0) or tiles, streams, kv heads (1)
   float* part;   // partial results [item - whole][split][row][d], then (m, l) pairs
   float2* part_ml;
 };
 
-// Item -> tile, kv head, stream.  Later tiles see more keys under a causal
-// mask: they come first.
+// Item -> tile, kv head, stream, tiles fastest: thread blocks that run at the
+// same time read the same keys.  Later tiles see more keys under a causal mask:
+// they come first.
 struct Item {
   int tile, h, s;
 };
 __device__ __forceinline__ Item item_of(const Params& pp, int item) {
   const Geom& g = pp.f.g;
+  const int rest = item / pp.q_tiles;
   Item r;
-  int rest;
-  if (pp.tile_slow) {
-    rest = item;
-    const int per_tile = g.streams * g.kv_heads;
-    r.tile = rest / per_tile;
-    rest -= r.tile * per_tile;
-  } else {
-    rest = item / pp.q_tiles;
-    r.tile = item - rest * pp.q_tiles;
-  }
-  r.tile = pp.q_tiles - 1 - r.tile;
+  r.tile = pp.q_tiles - 1 - (item - rest * pp.q_tiles);
   r.s = rest / g.kv_heads;
   r.h = rest - r.s * g.kv_heads;
   return r;
@@ -492,6 +483,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (j >= nblk) break;
       const uint32_t tS = tmem + lane_addr + (uint32_t)(acc * 128);
       ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&s_full[acc], acc_phase, wc);
+      // (this S follows P V of two units ago; seen here, a wait for the last P V below cannot mistake one for the other)
+      if (NB > 2 && i > 1) ok = ok && mbar_wait(&pv_done[w], i & 1, wc);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after();
@@ -780,8 +773,7 @@ Deal deal(const Geom& g, long long max_new) {
   }
   return d;
 }
-size_t part_rows(const Geom& g, long long max_new) {
-  const Deal d = deal(g, max_new);
+size_t part_rows(const Deal& d, const Geom& g, long long max_new) {
   return (size_t)(d.items - d.whole) * (d.splits == 1 ? 0 : d.splits) * rows_of(g, max_new);
 }
 
@@ -795,9 +787,8 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   p.q_tiles = tiles_of(f.g, f.max_new);
   p.whole = (int)d.whole;
   p.splits = d.splits;
-  p.tile_slow = 0;
   p.part = (float*)ws;
-  p.part_ml = (float2*)(p.part + part_rows(f.g, f.max_new) * D);
+  p.part_ml = (float2*)(p.part + part_rows(d, f.g, f.max_new) * D);
   CUtensorMap tk, tv;
   const char* err = nullptr;
   const long long heads = (long long)f.g.pages * f.g.kv_heads;
@@ -828,7 +819,8 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
 }  // namespace cache
 
 size_t cache_many_workspace(const cache::Geom& g, long long max_new) {
-  return cache::many::part_rows(g, max_new) * (g.d + 2) * sizeof(float);
+  using namespace cache::many;
+  return part_rows(deal(g, max_new), g, max_new) * (g.d + 2) * sizeof(float);
 }
 cudaError_t launch_cache_many(const cache::FwdParams& p, void* ws, cudaStream_t st) {
   using namespace cache::many;
