@@ -716,3 +716,50 @@ def test_plan_with_slots_of_many_tokens(streams, top):
         if p.step(new):
             assert p.step([-1] * streams) == 0
     _status_ok(p.V)
+
+
+def test_steps_captured_after_copies_and_across_streams():
+    """The launches depend on whatever is ahead of them in the stream: a copy, a
+    memset, another stream's work joined by an event, captured or not."""
+    f = Fwd(d=128, kv_heads=2, group=2, pt=32, steps=[(700, 1), (90, 1)], seed=16)
+    m = Fwd(d=64, kv_heads=2, group=1, pt=32, steps=[(400, 150)], seed=17)
+    want = [x.clone() for x in f.run()], [x.clone() for x in m.run()]
+    src = [x.q.clone() for x in (f, m)]
+    lens = f.dev["lens"].clone()
+    (o, lse, ws), (o2, lse2, ws2) = f.outputs(), m.outputs()
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        f.q.copy_(src[0])                                  # a kernel or a copy, then ours
+        f.dev["lens"].copy_(lens)                          # device-to-device copy
+        f.call(o, lse, ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            m.q.copy_(src[1])
+            ws2.zero_()
+            m.call(o2, lse2, ws2)
+        f.call(o, lse, ws)
+        main.wait_stream(side)
+        m.call(o2, lse2, ws2)                              # after both streams
+
+    def check():
+        torch.cuda.synchronize()
+        for got, ref in zip((o, lse, o2, lse2), (*want[0], *want[1])):
+            assert torch.equal(got, ref)
+
+    step()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for x in (f, m):
+            x.q.zero_()
+        f.dev["lens"].fill_(1)
+        o.fill_(7.5)                                       # rows behind the last stream are not written
+        o2.fill_(7.5)
+        graph.replay()
+        check()
+    del graph
+    _status_ok(f.V)
