@@ -377,6 +377,14 @@ def test_single_tokens(d, kv_heads, group, pt, steps):
     _check(d=d, kv_heads=kv_heads, group=group, pt=pt, steps=steps, seed=pt + group)
 
 
+@pytest.mark.parametrize("d,group,n", [(128, 1, 1), (64, 3, 2), (128, 5, 3), (64, 1, 16)])
+@pytest.mark.parametrize("length", [4000, 4400, 30000])
+def test_one_head_over_many_keys(d, group, n, length):
+    """One kv head whose keys all thread blocks share: few and many partial results."""
+    f = Fwd(d=d, kv_heads=1, group=group, pt=128, steps=[(length, n)], frame=1, seed=31)
+    f.check(*f.run())
+
+
 def test_many_streams():
     """More streams than a thread block has threads, most of them short, some idle."""
     steps = [(i * 53 % 90, 1 if i % 7 and i * 53 % 90 else 0) for i in range(700)] + [(3000, 1), (1, 1), (700, 1)]
