@@ -258,8 +258,10 @@ def test_append_skips_slots_outside_the_pool():
     was = _bytes_of(kc).clone()
     x = _bf16(rng, (4, 1, 128)).to(DEV)
     g = V.make_cache_geom(1, 1, 1, 128, 2, 16, 2)
+    V.vattn_cache_append(g, x, x, ints([-1, -5, -1, -2 ** 31]), kc, vc, ks, vs)       # skipped
+    _status_ok(V)
     V.vattn_cache_append(g, x, x, ints([32, -5, 2 ** 31 - 1, -2 ** 31]), kc, vc, ks, vs)
-    assert V.vattn_get_status() in (0, V.binding.VATTN_ERR_DEVICE_BOUNDS)
+    assert V.vattn_get_status() == V.binding.VATTN_ERR_DEVICE_BOUNDS
     assert torch.equal(was, _bytes_of(kc))
 
 

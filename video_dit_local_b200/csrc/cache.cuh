@@ -129,6 +129,7 @@ struct CacheAppendArgs {
   void* vc;
   float* ks;
   float* vs;
+  DevCtl ctl;
 };
 cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, cudaStream_t st);
 

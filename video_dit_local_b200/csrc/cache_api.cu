@@ -171,6 +171,7 @@ int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_st
   a.vc = vcache;
   a.ks = kscale;
   a.vs = vscale;
+  a.ctl = current_ctl();
   CHECK_LAUNCH(launch_cache_append(g, a, (cudaStream_t)stream), "cache_append launch");
   return ok();
 }

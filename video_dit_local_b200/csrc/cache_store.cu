@@ -276,7 +276,9 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const Geom g,
   const int n_slots = g.pages << g.page_shift;
   auto slot_at = [&](long long i) {
     const int x = i >= 0 && i < a.n_tokens ? __ldg(a.slots + i) : -1;
-    return x < n_slots ? x : -1;
+    if (x < n_slots) return x;
+    report_error(a.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
+    return -1;
   };
   const int my = slot_at(i0 + lane), before = slot_at(i0 - 1);
   const int up = __shfl_up_sync(~0u, my, 1), prev = lane == 0 ? before : up;
