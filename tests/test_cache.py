@@ -246,6 +246,7 @@ def test_refusals(V):
         (lambda: _fwd(V, g, scale=math.nan), INV),
         (lambda: _fwd(V, g, scale=math.inf), INV),
         (lambda: _fwd(V, g, max_new=-1), INV),
+        (lambda: _fwd(V, _geom(V, pages=0)), INV),
         (lambda: _fwd(V, g, q=Tok((5, 4, 64), [200, 64, 1], 16)), SHP),
         (lambda: _fwd(V, g, q=Tok((5, 4, 64), addr=20)), ALN),
         (lambda: _fwd(V, g, lse=20), ALN),

@@ -202,6 +202,7 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   if (max_new > n_tokens) max_new = n_tokens;
   if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
   if (g.streams == 0 || n_tokens == 0 || max_new == 0) return ok();
+  if (g.pages == 0) return fail(VATTN_ERR_INVALID_ARG, "pages must be > 0");
   if ((r = check_stride("q_stride", q_stride, g.q_heads, g.d))) return r;
   REQUIRE_PTR(q);
   REQUIRE_INTS(q_starts);
