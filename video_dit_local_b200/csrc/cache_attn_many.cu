@@ -66,6 +66,9 @@ struct Smem {
   // S accumulators (TMEM columns 128 b ..) and O accumulators (from column 128 NB, d columns a group).  At d = 64 a
   // third S fits: Q K^T then runs ahead of the softmax (see the MMA warp).
   static constexpr int NB = D == 64 ? 3 : 2;
+  // Barriers that say S is there: unit n's is n % NSB, which one group only waits for, and in each of its phases (at
+  // three accumulators the groups take turns with each).
+  static constexpr int NSB = NB % 2 ? 2 * NB : NB;
   static constexpr uint32_t O = 128 * NB;
   static constexpr int QK = 128 * D;            // 128 rows of bytes
   static constexpr int V = 128 * D * 2;         // 128 rows of f16
@@ -76,7 +79,7 @@ struct Smem {
   static constexpr int OFF_SC = OFF_V + NV * V;              // NS x Scales
   static constexpr int OFF_XCH = OFF_SC + NS * (int)sizeof(Scales);
   static constexpr int OFF_BAR = OFF_XCH + 4 * 128 * 8;      // [group][half][row] pairs of floats
-  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + 2 * NB + 2 + 1 + NS + 8;
+  static constexpr int NBAR = 1 + 3 * NK + 2 * NV + NSB + NB + 2 + 1 + NS + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int TOTAL = OFF_MISC + 16;
   static constexpr int ALLOC = TOTAL + 1024;
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const Params pp) {
   using L = Smem<D, TWO>;
-  constexpr int NK = L::NK, NB = L::NB;
+  constexpr int NK = L::NK, NB = L::NB, NSB = L::NSB;
   constexpr int ROWS = L::TILES * BM;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* v8_empty = k_empty + NK; // V's bytes of a stage are converted
   uint64_t* v_full = v8_empty + NK;
   uint64_t* v_empty = v_full + NV;
-  uint64_t* s_full = v_empty + NV;   // S of an accumulator is in TMEM
-  uint64_t* p_full = s_full + NB;    // ... and its P
+  uint64_t* s_full = v_empty + NV;   // S of a unit is in TMEM
+  uint64_t* p_full = s_full + NSB;   // P of an accumulator is
   uint64_t* pv_done = p_full + NB;   // a group's last P V is done (three S accumulators)
   uint64_t* o_final = pv_done + 2;
   uint64_t* sc_full = o_final + 1;
@@ -241,10 +244,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&v_full[i], V_WARPS);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < NB; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
-    }
+    for (int i = 0; i < NSB; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < NB; ++i) mbar_init(&p_full[i], 8);
     for (int i = 0; i < 2; ++i) mbar_init(&pv_done[i], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&max_full[i], 2);
     mbar_init(o_final, 1);
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int kk = 0; kk < D / 32; ++kk)
             mma_ss_e4m3(tmem + (uint32_t)(b * 128), desc_bytes<D>(qb + part * L::QK + kk * 32),
                         desc_bytes<D>(kb + kk * 32), idesc_e4m3_f32(BM, BN), part + kk > 0);
-        tc_commit(&s_full[b]);
+        tc_commit(&s_full[n % NSB]);
         if (!TWO || w == 1) tc_commit(&k_empty[sg]);
         return true;
       };
@@ -491,23 +492,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float* other_max = (float*)xch + (w * 2 + 1 - half) * 256 + row;
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
-    int acc = w;            // S accumulator of the group's unit 2 i + w ...
-    uint32_t acc_phase = 0; // ... and the parity of its use
+    int sb = w;             // barrier of the S of the group's unit 2 i + w ...
+    uint32_t s_phase = 0;   // ... and the parity of its phase
     auto next_unit = [&] {
-      acc += 2;
-      if (acc >= NB) {
-        acc -= NB;
-        acc_phase ^= 1u;
+      sb += 2;
+      if (sb >= NSB) {
+        sb -= NSB;
+        s_phase ^= 1u;
       }
     };
     for (int i = 0;; ++i, next_unit()) {
       const int j = TWO ? i : 2 * i + w;
       if (j >= nblk) break;
+      const int acc = sb < NB ? sb : sb - NB;  // S accumulator: the unit modulo NB
       const uint32_t tS = tmem + lane_addr + (uint32_t)(acc * 128);
-      ok = mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&s_full[acc], acc_phase, wc);
-      // (this S follows P V of two units ago; seen here, a wait for the last P V below cannot mistake one for the other)
-      if (NB > 2 && i > 1) ok = ok && mbar_wait(&pv_done[w], i & 1, wc);
-      ok = __all_sync(~0u, ok);
+      ok = __all_sync(~0u, mbar_wait(&sc_full[j % NS], (j / NS) & 1, wc) && mbar_wait(&s_full[sb], s_phase, wc));
       if (!ok) break;
       tc_fence_after();
       if (idle) {
@@ -588,15 +587,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tmem_st16(tS + half * 32 + q2 * 16, pk);
       }
+      // Three accumulators: the group's last P V, waited for here by every unit whether O is rescaled or not.  A wait
+      // knows a phase by its parity, so it has to come while that phase is the one under way or the last one
+      // complete: P V of this unit cannot complete before this warp's arrival on p_full below, and the unit before
+      // has waited for the phase before this one.  (It is done by now: the softmax of a unit takes longer.)
+      if (NB > 2 && i > 0) {
+        ok = __all_sync(~0u, mbar_wait(&pv_done[w], (i - 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+      }
       if (__any_sync(~0u, need)) {
         // O of this group is quiescent: the commit that signalled this S also
-        // covers the previous P V into it (two accumulators; with three it is
+        // covers the previous P V into it (two accumulators; with three it was
         // waited for), and the next one waits for p_full.
-        if (NB > 2 && i > 0) {
-          ok = __all_sync(~0u, mbar_wait(&pv_done[w], (i - 1) & 1, wc));
-          if (!ok) break;
-          tc_fence_after();
-        }
 #pragma unroll 1
         for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
