@@ -405,7 +405,8 @@ enum {
   VATTN_PLAN_NO_PAGES = 1,    /* the pool has too few free pages */
   VATTN_PLAN_TABLE_FULL = 2,  /* a stream outgrows its block_table row */
   VATTN_PLAN_NO_SLOTS = 3,    /* more new tokens than max_tokens */
-  VATTN_PLAN_BAD_STATE = 4    /* a length, count or page id that cannot be */
+  VATTN_PLAN_BAD_STATE = 4    /* a length, count or page id that cannot be: of the page ids, those that the step
+                                 gives back, hands out or goes on filling are checked */
 };
 
 /* Plans one step of every stream on the device: gives each stream the pages

@@ -29,11 +29,13 @@ def plan(page_tokens, width, pages, new_tokens, kv_lens, table, free_pages, n_fr
                 [-1] * max_tokens, [status, 0, n_free, max([0, *map(int, kv_lens)])])
 
     worst = 0
-    for n, old in zip(new_tokens, lens):
+    for s, (n, old) in enumerate(zip(new_tokens, lens)):
         if old < 0 or old > width * page_tokens:
             worst = max(worst, 4)
         elif n >= 0 and old + n > width * page_tokens:
             worst = max(worst, 2)
+        elif n > 0 and old % page_tokens and not 0 <= table[s, old // page_tokens] < pages:
+            worst = 4                    # the page that the stream goes on filling
     if worst:
         return stop(worst)
     stack = [int(x) for x in free[:max(n_free, 0)]]
@@ -43,7 +45,7 @@ def plan(page_tokens, width, pages, new_tokens, kv_lens, table, free_pages, n_fr
                 if not 0 <= table[s, j] < pages:
                     return stop(4)
                 stack.append(int(table[s, j]))
-    if n_free < 0 or len(stack) > pages:
+    if not 0 <= n_free <= pages or len(stack) > pages:
         return stop(4)
     if sum(max(0, int(n)) for n in new_tokens) > max_tokens:
         return stop(3)
@@ -51,6 +53,8 @@ def plan(page_tokens, width, pages, new_tokens, kv_lens, table, free_pages, n_fr
     need = sum(-(-(old + n) // page_tokens) - -(-old // page_tokens) for n, old in zip(new_tokens, lens) if n >= 0)
     if need > len(stack):
         return stop(1)
+    if not all(0 <= x < pages for x in stack[len(stack) - need:]):
+        return stop(4)
     starts, slots = [0], []
     for s, n in enumerate(new_tokens):
         old, n = lens[s], int(n)

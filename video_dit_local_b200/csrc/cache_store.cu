@@ -12,6 +12,8 @@ namespace cache {
 //   free[n_free + G_s + j] = table[s][j]                (s ends, j < have)
 //   table[s][have + j] = free[n_free + G - 1 - T_s - j] (j < pages taken)
 //   slot of token t of stream s: position len + t - Q_s in its pages.
+// Every page id that a stream gives, takes or goes on filling is checked before
+// the state changes.
 // Bound by the latency of its handful of dependent reads, so one thread block
 // does it all with one scan: a thread sums a run of streams, the block scans the
 // threads' sums, and pages (and the slots of few tokens) are dealt out to all
@@ -53,22 +55,20 @@ __device__ __forceinline__ int last_at_most(const T* first, int n, int x) {
 }
 
 __device__ __forceinline__ int slot_of(const Geom& g, const int* table, int s, int pos) {
-  const int page = table[(long long)s * g.width + (pos >> g.page_shift)];
-  return (unsigned)page < (unsigned)g.pages ? (page << g.page_shift) + (pos & (g.page_tokens - 1)) : -1;
+  return (table[(long long)s * g.width + (pos >> g.page_shift)] << g.page_shift) + (pos & (g.page_tokens - 1));
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const CachePlanArgs a, int list_slots) {
   __shared__ long long warp_give[32], warp_take[32], warp_add[32];
   __shared__ int warp_longest[32], warp_worst[32];
   __shared__ int give0[PLAN_THREADS], take0[PLAN_THREADS], add0[PLAN_THREADS];
-  __shared__ int bad_page;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const long long cap = (long long)g.width << g.page_shift;
   const int n_free = *a.n_free;
   const int per = (g.streams + PLAN_THREADS - 1) / PLAN_THREADS;
   const int s0 = min(t * per, g.streams), s1 = min(s0 + per, g.streams);
-  if (t == 0) bad_page = 0;
+  auto in_pool = [&](int page) { return (unsigned)page < (unsigned)g.pages; };
 
   // sums and the verdict, before anything is written
   long long give = 0, take = 0, add = 0;
@@ -85,6 +85,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const 
       take += r.take;
       add += r.add;
       longest = max(longest, n < 0 ? 0 : len + r.add);
+      // the page that the stream goes on filling
+      if (r.add > 0 && (len & (g.page_tokens - 1)) && !in_pool(a.table[(long long)s * g.width + (len >> g.page_shift)]))
+        worst = VATTN_PLAN_BAD_STATE;
     }
   }
   const long long my_give = give, my_take = take, my_add = add;
@@ -144,18 +147,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const 
   add0[t] = (int)add;
   __syncthreads();
 
-  if (verdict == VATTN_PLAN_OK && tot_give > 0) {
+  if (verdict == VATTN_PLAN_OK) {
+    bool bad = false;
+    // what is taken from below the pages that ending streams give
+    for (int i = (int)tot_give + t; i < (int)tot_take; i += PLAN_THREADS)
+      bad |= !in_pool(a.free_pages[n_free + (int)tot_give - 1 - i]);
     // pages of ending streams onto the stack: above its top, so nothing is lost if one turns out bad
     for (int i = t; i < (int)tot_give; i += PLAN_THREADS) {
       const int u = last_at_most(give0, PLAN_THREADS, i);
       int s = u * per, j = i - give0[u];
       for (int x; j >= (x = stream_plan(g, a, s).give); ++s) j -= x;
       const int page = a.table[(long long)s * g.width + j];
-      if ((unsigned)page >= (unsigned)g.pages) bad_page = 1;
+      bad |= !in_pool(page);
       a.free_pages[n_free + i] = page;
     }
-    __syncthreads();
-    if (bad_page) verdict = VATTN_PLAN_BAD_STATE;
+    if (__syncthreads_or(bad)) verdict = VATTN_PLAN_BAD_STATE;
   }
   if (verdict != VATTN_PLAN_OK) {
     int top = 0;
