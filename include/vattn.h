@@ -442,9 +442,13 @@ int vattn_cache_plan(const vattn_cache_geom* geom, const int32_t* new_tokens, co
  * subnormals.  A token whose k or v row of a kv head holds a NaN or an infinity
  * is stored as NaN keys and zero values for that head: outputs that see it are
  * NaN, all others are untouched.
- * slots: as vattn_cache_plan lists them: ascending within a 16-token block,
- * and a block's new tokens directly follow those that it holds; negative
- * entries are skipped.  A slot must not be listed twice. */
+ * slots: as vattn_cache_plan lists them: a 16-token block's new tokens are
+ * adjacent in the list (no negative entry and no other block's token between
+ * them), ascending by one, and directly follow those that the block holds.
+ * Negative entries are skipped.  A slot must not be listed twice, nor a block
+ * come back to: such tokens are not stored and VATTN_ERR_DEVICE_BOUNDS is
+ * recorded where the block's earlier tokens are among the 32 entries before;
+ * farther apart, the contents of that block are unspecified. */
 int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_stride, const void* v,
                        int64_t v_stride, const int32_t* slots, int64_t n_tokens, void* kcache, void* vcache,
                        float* kscale, float* vscale, void* stream);

@@ -93,15 +93,19 @@ def scale_exponent(absmax):
 
 
 def append(k, v, slots, kc, vc, ks, vs):
-    """k, v float64 [n, heads, d]; kc, vc the values of the cache's bytes [pages, heads, page_tokens, d]; returns new arrays."""
+    """k, v float64 [n, heads, d]; kc, vc the values of the cache's bytes [pages, heads, page_tokens, d]; returns new arrays.
+    Lists that come back to a block raise ValueError."""
     kc, vc, ks, vs = kc.copy(), vc.copy(), ks.copy(), vs.copy()
     n, heads, _ = k.shape
     page_tokens = kc.shape[2]
-    i = 0
+    i, met = 0, set()
     while i < n:
         if slots[i] < 0:
             i += 1
             continue
+        if slots[i] // SCALE_TOKENS in met:
+            raise ValueError(f"slot {slots[i]}: the list comes back to its block")
+        met.add(slots[i] // SCALE_TOKENS)
         j = i + 1
         while j < n and slots[j] == slots[j - 1] + 1 and slots[j] % SCALE_TOKENS:
             j += 1

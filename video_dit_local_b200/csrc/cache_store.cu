@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const Geom g,
     report_error(a.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
     return -1;
   };
-  const int my = slot_at(i0 + lane), before = slot_at(i0 - 1);
-  const int up = __shfl_up_sync(~0u, my, 1), prev = lane == 0 ? before : up;
+  const int my = slot_at(i0 + lane), earlier = slot_at(i0 - 32 + lane);
+  const int before = __shfl_sync(~0u, earlier, 31), up = __shfl_up_sync(~0u, my, 1), prev = lane == 0 ? before : up;
   // a block belongs to the first of its new tokens
   uint32_t leads = __ballot_sync(~0u, lane < span && my >= 0 && !(prev >= 0 && prev + 1 == my && (my & 15) != 0));
   for (; leads; leads &= leads - 1) {
@@ -295,6 +295,11 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const Geom g,
     const int slot = __shfl_sync(~0u, my, lead);
     const long long i = i0 + lead;
     const int held = slot & 15;
+    // a block that the list comes back to after a gap (or a slot listed twice): another warp writes it
+    if (__any_sync(~0u, (earlier >> 4) == (slot >> 4) || (lane < lead && (my >> 4) == (slot >> 4)))) {
+      report_error(a.ctl.err_word, VATTN_ERR_DEVICE_BOUNDS);
+      continue;
+    }
     // its new tokens: consecutive slots from there on
     const bool same = lane >= lead && lane - lead + held < 16 && my == slot + lane - lead;
     const int n = __ffs(~(__ballot_sync(~0u, same) >> lead)) - 1;
