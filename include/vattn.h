@@ -469,7 +469,9 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
                     const float* kscale, const float* vscale, float scale, int64_t n_tokens, int64_t max_new,
                     void* o, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
-/* Scratch bytes that vattn_cache_fwd needs. */
+/* Scratch bytes that vattn_cache_fwd needs for any call of this geometry with
+ * up to n_tokens and max_new: a workspace sized for the longest step serves the
+ * shorter ones too. */
 int vattn_cache_workspace_size(const vattn_cache_geom* geom, int64_t n_tokens, int64_t max_new, size_t* bytes);
 
 /* Scratch bytes that `op` needs for `geom` (0 if none). */

@@ -140,6 +140,7 @@ cudaError_t launch_cache_few(const cache::FwdParams& p, void* workspace, cudaStr
 
 // -- cache_attn_many.cu --
 size_t cache_many_workspace(const cache::Geom& g, long long max_new);
+size_t cache_many_workspace_most(const cache::Geom& g, long long max_new);  // of any max_new up to this one
 cudaError_t launch_cache_many(const cache::FwdParams& p, void* workspace, cudaStream_t st);
 
 // 3-D map over e4m3 cache pages [pages * kv_heads][page_tokens][d]: box = one

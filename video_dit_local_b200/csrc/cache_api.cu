@@ -1,5 +1,6 @@
 // C-ABI entry points of the 8-bit key/value cache: argument validation and
 // launches on the caller's stream.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -99,6 +100,13 @@ size_t fwd_workspace(const cache::Geom& g, int64_t max_new) {
   if (g.streams == 0 || max_new == 0) return 0;
   return cache_few_fits(g, max_new) ? cache_few_workspace(g) : cache_many_workspace(g, max_new);
 }
+// What serves every max_new up to this one: fewer tokens can need more (one
+// kernel always leaves partial results, the other only where items are few).
+size_t fwd_workspace_most(const cache::Geom& g, int64_t max_new) {
+  if (g.streams == 0 || max_new == 0) return 0;
+  const size_t few = cache_few_fits(g, 1) ? cache_few_workspace(g) : 0;
+  return cache_few_fits(g, max_new) ? few : std::max(few, cache_many_workspace_most(g, max_new));
+}
 
 }  // namespace
 }  // namespace vattn
@@ -185,7 +193,7 @@ int vattn_cache_workspace_size(const vattn_cache_geom* geom, int64_t n_tokens, i
   if (!bytes) return fail(VATTN_ERR_INVALID_ARG, "bytes is NULL");
   if (max_new > n_tokens) max_new = n_tokens;
   if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
-  *bytes = fwd_workspace(g, max_new);
+  *bytes = fwd_workspace_most(g, max_new);
   return ok();
 }
 

@@ -764,14 +764,14 @@ int tiles_of(const Geom& g, long long max_new) {
 //    token-causal queries over 9000 keys, 24 heads: 355 us, 469 unsplit).
 //  - Else all items get the same number of splits: enough that the last ones
 //    to finish are short, counting half the tiles as there.
+constexpr int SMS = 148, MOST = SMS * 8;  // MOST bounds the partial results
 struct Deal {
   long long items, whole;
   int splits;
 };
-Deal deal(const Geom& g, long long max_new) {
-  constexpr int SMS = 148, MOST = SMS * 8;  // MOST bounds the partial results
+Deal deal(const Geom& g, long long tiles) {
   Deal d;
-  d.items = (long long)g.streams * g.kv_heads * tiles_of(g, max_new);
+  d.items = (long long)g.streams * g.kv_heads * tiles;
   d.whole = d.items;
   d.splits = 1;
   const double blocks = std::max(1.0, (double)g.width * g.page_tokens / BN * (g.streams == 1 ? 1.0 : 0.5));
@@ -784,11 +784,12 @@ Deal deal(const Geom& g, long long max_new) {
     }
   };
   if (g.streams == 1) {
-    const long long waves = d.items / SMS;
-    for (long long w = std::max(0ll, waves - 2); w <= waves; ++w) {
+    // (costs count from the first of these waves on, so that the choice is the same whatever number comes before)
+    const long long waves = d.items / SMS, w0 = std::max(0ll, waves - 2);
+    for (long long w = w0; w <= waves; ++w) {
       const long long rest = d.items - w * SMS;
       for (int sp = 1; sp == 1 || (sp <= 64 && rest * sp <= MOST); ++sp)
-        take(w * SMS, sp, w * (blocks + 3) + (double)((rest * sp + SMS - 1) / SMS) * (blocks / sp + (sp == 1 ? 3 : 6)));
+        take(w * SMS, sp, (double)(w - w0) * (blocks + 3) + (double)((rest * sp + SMS - 1) / SMS) * (blocks / sp + (sp == 1 ? 3 : 6)));
     }
   } else {
     for (int sp = 1; sp == 1 || (sp <= 64 && d.items * sp <= MOST); ++sp) {
@@ -798,13 +799,15 @@ Deal deal(const Geom& g, long long max_new) {
   }
   return d;
 }
-size_t part_rows(const Deal& d, const Geom& g, long long max_new) {
-  return (size_t)(d.items - d.whole) * (d.splits == 1 ? 0 : d.splits) * rows_of(g, max_new);
+size_t part_rows(const Deal& d, int rows) {
+  return (size_t)(d.items - d.whole) * (d.splits == 1 ? 0 : d.splits) * rows;
 }
+size_t bytes_of(const Geom& g, size_t part_rows) { return part_rows * (g.d + 2) * sizeof(float); }
 
 template <int D, bool TWO>
 cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
-  const Deal d = deal(f.g, f.max_new);
+  const int rows = rows_of(f.g, f.max_new);
+  const Deal d = deal(f.g, tiles_of(f.g, f.max_new));
   const long long grid = d.whole + (d.items - d.whole) * d.splits;
   if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
   Params p;
@@ -813,7 +816,7 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   p.whole = (int)d.whole;
   p.splits = d.splits;
   p.part = (float*)ws;
-  p.part_ml = (float2*)(p.part + part_rows(d, f.g, f.max_new) * D);
+  p.part_ml = (float2*)(p.part + part_rows(d, rows) * D);
   CUtensorMap tk, tv;
   const char* err = nullptr;
   const long long heads = (long long)f.g.pages * f.g.kv_heads;
@@ -827,7 +830,6 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   kernel<<<(unsigned)grid, THREADS, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || d.whole == d.items) return e;
-  const int rows = rows_of(f.g, f.max_new);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(d.items - d.whole), (unsigned)(rows / 8));
   cfg.blockDim = dim3(256);
@@ -845,7 +847,22 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
 
 size_t cache_many_workspace(const cache::Geom& g, long long max_new) {
   using namespace cache::many;
-  return part_rows(deal(g, max_new), g, max_new) * (g.d + 2) * sizeof(float);
+  return bytes_of(g, part_rows(deal(g, tiles_of(g, max_new)), rows_of(g, max_new)));
+}
+size_t cache_many_workspace_most(const cache::Geom& g, long long max_new) {
+  using namespace cache::many;
+  size_t most = 0;
+  const long long one = std::min<long long>(max_new, BM / g.group);  // the most tokens of one tile of BM rows
+  if (one > 0 && !cache_few_fits(g, one)) most = part_rows(deal(g, 1), BM);
+  if (max_new * g.group <= BM) return bytes_of(g, most);
+  // Tiles of 2 BM rows.  Several streams: none is split once two splits of each item are too many.  One stream: the
+  // choice depends on what is left after whole waves, and from three waves on 148 tiles show every remainder.
+  const long long per_tile = (long long)g.streams * g.kv_heads;
+  long long last = tiles_of(g, max_new);
+  last = std::min(last, g.streams > 1 ? MOST / 2 / per_tile : (2 * SMS - 1) / per_tile + 1 + SMS);
+  for (long long tiles = tiles_of(g, BM / g.group + 1); tiles <= last; ++tiles)
+    most = std::max(most, part_rows(deal(g, tiles), 2 * BM));
+  return bytes_of(g, most);
 }
 cudaError_t launch_cache_many(const cache::FwdParams& p, void* ws, cudaStream_t st) {
   using namespace cache::many;
