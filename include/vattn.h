@@ -463,7 +463,8 @@ int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_st
  *   workspace >= vattn_cache_workspace_size(geom, n_tokens, max_new): partial
  *     results of keys that are split over several thread blocks.  Two calls
  *     that may overlap on the GPU need a workspace each.
- * A query row with a NaN or an infinity gives a NaN row.  Deterministic. */
+ * A query row with a NaN or an infinity gives a NaN row, unless it sees nothing.
+ * Deterministic. */
 int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_stride, const int32_t* q_starts,
                     const int32_t* kv_lens, const int32_t* block_table, const void* kcache, const void* vcache,
                     const float* kscale, const float* vscale, float scale, int64_t n_tokens, int64_t max_new,

@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         a1 = w == 0 ? a_other : a_self;
         both = nblk >= 2;
       }
-      l += poison;
+      if (lo < hi) l += poison;  // (a row that sees nothing stays empty whatever its query)
       const float norm = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
       a0 *= norm;
       a1 *= norm;
