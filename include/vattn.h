@@ -384,8 +384,11 @@ int vattn_dual_bwd(const vattn_geom* geom, const void* q, const void* k, const v
  *
  * Limits (VATTN_ERR_UNSUPPORTED otherwise): head_dim 64 or 128, page_tokens 16,
  * 32, 64 or 128, q_heads and streams <= 65535; pages * page_tokens, pages *
- * kv_heads, streams * kv_heads, n_tokens and max_new * q_heads / kv_heads below
- * 2^31, table_width * page_tokens below 2^31 - 256.  Indices that the kernels read from device memory (q_starts, kv_lens,
+ * kv_heads, streams * kv_heads, n_tokens, max_tokens and the rows max_new *
+ * q_heads / kv_heads below 2^31, as streams * kv_heads times the tiles of 256
+ * rows; table_width * page_tokens below 2^31 - 256; n_tokens * kv_heads of an
+ * append below 2^34.
+ * Indices that the kernels read from device memory (q_starts, kv_lens,
  * block_table, slots) are checked there: one out of range is never
  * dereferenced, VATTN_ERR_DEVICE_BOUNDS is recorded (vattn_get_status) and the
  * outputs of the stream concerned are unspecified.

@@ -139,6 +139,7 @@ size_t cache_few_workspace(const cache::Geom& g);
 cudaError_t launch_cache_few(const cache::FwdParams& p, void* workspace, cudaStream_t st);
 
 // -- cache_attn_many.cu --
+long long cache_many_items(const cache::Geom& g, long long max_new);  // thread blocks, before any is split
 size_t cache_many_workspace(const cache::Geom& g, long long max_new);
 size_t cache_many_workspace_most(const cache::Geom& g, long long max_new);  // of any max_new up to this one
 cudaError_t launch_cache_many(const cache::FwdParams& p, void* workspace, cudaStream_t st);

@@ -88,6 +88,14 @@ int check_tokens(int64_t n_tokens) {
   return VATTN_OK;
 }
 
+// Query rows of a call: every stream may have max_new tokens.
+int check_rows(const cache::Geom& g, int64_t max_new) {
+  if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
+  if (cache_many_items(g, max_new) >= (1ll << 31))
+    return fail(VATTN_ERR_UNSUPPORTED, "streams * kv_heads * tiles of 256 query rows >= 2^31");
+  return VATTN_OK;
+}
+
 int check_stride(const char* name, int64_t stride, int64_t heads, int64_t d) {
   if (stride < heads * d)
     return fail(VATTN_ERR_SHAPE, "%s %lld is less than heads * head_dim = %lld", name, (long long)stride,
@@ -158,6 +166,7 @@ int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_st
   int r = build_geom(geom, &g);
   if (r) return r;
   if ((r = check_tokens(n_tokens))) return r;
+  if (n_tokens * g.kv_heads >= (1ll << 34)) return fail(VATTN_ERR_UNSUPPORTED, "n_tokens * kv_heads must be < 2^34");
   if (n_tokens == 0) return ok();
   if ((r = check_stride("k_stride", k_stride, g.kv_heads, g.d))) return r;
   if ((r = check_stride("v_stride", v_stride, g.kv_heads, g.d))) return r;
@@ -192,7 +201,7 @@ int vattn_cache_workspace_size(const vattn_cache_geom* geom, int64_t n_tokens, i
   if (max_new < 0) return fail(VATTN_ERR_INVALID_ARG, "max_new must be >= 0");
   if (!bytes) return fail(VATTN_ERR_INVALID_ARG, "bytes is NULL");
   if (max_new > n_tokens) max_new = n_tokens;
-  if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
+  if ((r = check_rows(g, max_new))) return r;
   *bytes = fwd_workspace_most(g, max_new);
   return ok();
 }
@@ -208,7 +217,7 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   if (max_new < 0) return fail(VATTN_ERR_INVALID_ARG, "max_new must be >= 0");
   if (!(scale > 0.f) || std::isinf(scale)) return fail(VATTN_ERR_INVALID_ARG, "scale must be positive and finite");
   if (max_new > n_tokens) max_new = n_tokens;
-  if (max_new * g.group >= (1ll << 31)) return fail(VATTN_ERR_UNSUPPORTED, "max_new * query heads per kv head >= 2^31");
+  if ((r = check_rows(g, max_new))) return r;
   if (g.streams == 0 || n_tokens == 0 || max_new == 0) return ok();
   if (g.pages == 0) return fail(VATTN_ERR_INVALID_ARG, "pages must be > 0");
   if ((r = check_stride("q_stride", q_stride, g.q_heads, g.d))) return r;

@@ -808,8 +808,7 @@ template <int D, bool TWO>
 cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
   const int rows = rows_of(f.g, f.max_new);
   const Deal d = deal(f.g, tiles_of(f.g, f.max_new));
-  const long long grid = d.whole + (d.items - d.whole) * d.splits;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  const long long grid = d.whole + (d.items - d.whole) * d.splits;  // the items, or few more than MOST
   Params p;
   p.f = f;
   p.q_tiles = tiles_of(f.g, f.max_new);
@@ -845,6 +844,9 @@ cudaError_t launch(const FwdParams& f, void* ws, cudaStream_t stream) {
 }  // namespace many
 }  // namespace cache
 
+long long cache_many_items(const cache::Geom& g, long long max_new) {
+  return (long long)g.streams * g.kv_heads * cache::many::tiles_of(g, max_new);
+}
 size_t cache_many_workspace(const cache::Geom& g, long long max_new) {
   using namespace cache::many;
   return bytes_of(g, part_rows(deal(g, tiles_of(g, max_new)), rows_of(g, max_new)));

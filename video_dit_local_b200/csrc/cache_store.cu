@@ -232,9 +232,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const 
 
 // Slots of many new tokens, from the tables and lengths that plan_kernel left.
 __global__ void __launch_bounds__(256) slots_kernel(const Geom g, const CachePlanArgs a) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
+  const unsigned at = blockIdx.x * 256 + threadIdx.x;  // up to 255 past max_tokens, which may be 2^31 - 1
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (t >= a.max_tokens) return;
+  if (at >= (unsigned)a.max_tokens) return;
+  const int t = (int)at;
   int slot = -1;
   if (t < a.q_starts[g.streams]) {
     const int s = last_at_most(a.q_starts, g.streams, t);
@@ -428,7 +429,7 @@ cudaError_t launch_cache_plan(const cache::Geom& g, const CachePlanArgs& a, cuda
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || few) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.max_tokens + 255) / 256);
+  cfg.gridDim = dim3(((unsigned)a.max_tokens + 255) / 256);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -449,7 +450,6 @@ cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, 
   const int span = (long long)a.n_tokens / 16 * g.kv_heads >= 148 * 16 ? 16 : 1;
   const long long warps = (long long)((a.n_tokens + span - 1) / span) * g.kv_heads;
   const long long blocks = (warps + APPEND_WARPS - 1) / APPEND_WARPS;
-  if (warps >= (1ll << 31)) return cudaErrorInvalidValue;
   if (g.d == 128)
     append_kernel<128><<<(int)blocks, APPEND_WARPS * 32, 0, st>>>(g, a, span);
   else
