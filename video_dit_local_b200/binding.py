@@ -398,7 +398,7 @@ def _tokens(x, what: str, dev: int):
         raise ValueError(f"{what} is on another device than the call's other tensors")
     n, heads, d = x.shape
     token, head, channel = x.stride()
-    if channel != 1 or head != d:
+    if channel != 1 or (head != d and heads > 1):
         raise ValueError(f"{what}: heads and channels of a token must be contiguous")
     return x.data_ptr(), token if n > 1 else heads * d, n
 
