@@ -368,19 +368,39 @@ def vattn_workspace_size(op: int, geom: Geom) -> int:
 
 # The cache calls are short enough for their argument checks to matter, so each
 # tensor is looked at once.
+_torch = None
+_I32 = _F32 = _BF16 = _BYTES = ()  # what an array's elements may be; known once a call has met a tensor
+
+
+def _use_torch() -> None:
+    global _torch, _I32, _F32, _BF16, _BYTES
+    import torch
+    _I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+    _BYTES = (torch.float8_e4m3fn, torch.uint8)
+    _torch = torch
+
+
 def _device(x) -> int:
     """The device of a call's first tensor; it must be the current one, on whose stream the kernels run."""
     dev = x.get_device()
     if dev < 0:
         raise ValueError("a device pointer argument got a host tensor: pass a CUDA tensor")
-    import torch
-    if torch.cuda.is_initialized() and dev != torch.cuda.current_device():
+    if _torch is None:
+        _use_torch()
+    cuda = _torch.cuda
+    if cuda.is_initialized() and dev != cuda.current_device():
         raise ValueError(f"tensors on device {dev}: all must be on the current device")
     return dev
 
 
-def _on(x, dev: int) -> Optional[int]:
-    """Address of a contiguous tensor on device `dev`; None and raw addresses pass."""
+def _on(x, dev: int, what: str, kind, size: int) -> Optional[int]:
+    """Address of a contiguous tensor on device `dev` of `size` bytes or more, its type one of `kind`; None and raw
+    addresses pass."""
+    try:
+        if x.get_device() == dev and x.is_contiguous() and x.dtype in kind and x.nbytes >= size:
+            return x.data_ptr()
+    except AttributeError:  # no tensor
+        pass
     if x is None or isinstance(x, int):
         return x
     if x.get_device() != dev:
@@ -388,15 +408,22 @@ def _on(x, dev: int) -> Optional[int]:
                          f"tensors on devices {dev} and {x.get_device()}: all must be on the current device")
     if not x.is_contiguous():
         raise ValueError("tensor arguments must be contiguous (the library reads them as dense arrays)")
+    if hasattr(x, "dtype"):
+        raise ValueError(f"{what}: {x.nbytes} bytes of {x.dtype}, but the call needs {size} of {kind[0]}")
     return x.data_ptr()
 
 
-def _tokens(x, what: str, dev: int):
-    """(address, token stride, tokens) of a [tokens, heads, d] tensor whose tokens'
+def _tokens(x, what: str, dev: int, heads: int, d: int):
+    """(address, token stride, tokens) of a bf16 [tokens, heads, d] tensor whose tokens'
     rows are dense (a slice of a fused projection along dim 1 is)."""
     if x.get_device() != dev:
         raise ValueError(f"{what} is on another device than the call's other tensors")
-    n, heads, d = x.shape
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{what}: shape {tuple(shape)}, but the geometry says [tokens, {heads}, {d}]")
+    if getattr(x, "dtype", _BF16[0]) not in _BF16:
+        raise ValueError(f"{what}: {x.dtype}, but the call needs {_BF16[0]}")
+    n = shape[0]
     token, head, channel = x.stride()
     if channel != 1 or (head != d and heads > 1):
         raise ValueError(f"{what}: heads and channels of a token must be contiguous")
@@ -406,31 +433,44 @@ def _tokens(x, what: str, dev: int):
 def _current_stream(stream, dev: int) -> int:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    if _torch is None:
+        _use_torch()
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def vattn_cache_plan(geom: CacheGeom, new_tokens, kv_lens, block_table, free_pages, n_free, kv_lens_out, n_free_out,
                      q_starts, slots, result, max_tokens: Optional[int] = None, stream=None) -> None:
     """Pages and slots of one step's new tokens (int32 tensors; max_tokens defaults to the length of slots)."""
     dev = -1 if isinstance(new_tokens, int) else _device(new_tokens)
-    _check(lib.vattn_cache_plan(ctypes.byref(geom), _on(new_tokens, dev), _on(kv_lens, dev), _on(block_table, dev),
-                                _on(free_pages, dev), _on(n_free, dev), _on(kv_lens_out, dev), _on(n_free_out, dev),
-                                _on(q_starts, dev), _on(slots, dev),
-                                slots.numel() if max_tokens is None else max_tokens, _on(result, dev),
-                                _current_stream(stream, dev)))
+    if max_tokens is None:
+        max_tokens = slots.numel()
+    i32, lens = _I32, geom.streams * 4
+    code = lib.vattn_cache_plan(geom, _on(new_tokens, dev, "new_tokens", i32, lens), _on(kv_lens, dev, "kv_lens", i32, lens),
+                                _on(block_table, dev, "block_table", i32, lens * geom.table_width),
+                                _on(free_pages, dev, "free_pages", i32, geom.pages * 4),
+                                _on(n_free, dev, "n_free", i32, 4), _on(kv_lens_out, dev, "kv_lens_out", i32, lens),
+                                _on(n_free_out, dev, "n_free_out", i32, 4), _on(q_starts, dev, "q_starts", i32, lens + 4),
+                                _on(slots, dev, "slots", i32, max_tokens * 4), max_tokens,
+                                _on(result, dev, "result", i32, 16), _current_stream(stream, dev))
+    if code:
+        _check(code)
 
 
 def vattn_cache_append(geom: CacheGeom, k, v, slots, kcache, vcache, kscale, vscale, stream=None) -> None:
     """Quantise k, v [tokens, kv_heads, d] (bf16, may be slices of a fused projection) into their slots."""
     dev = _device(k)
-    kp, ks, n = _tokens(k, "k", dev)
-    vp, vs, nv = _tokens(v, "v", dev)
-    if nv != n or slots.numel() < n:
-        raise ValueError(f"{n} keys, {nv} values and {slots.numel()} slots")
-    _check(lib.vattn_cache_append(ctypes.byref(geom), kp, ks, vp, vs, _on(slots, dev), n, _on(kcache, dev),
-                                  _on(vcache, dev), _on(kscale, dev), _on(vscale, dev),
-                                  _current_stream(stream, dev)))
+    heads, d = geom.kv_heads, geom.head_dim
+    kp, ks, n = _tokens(k, "k", dev, heads, d)
+    vp, vs, nv = _tokens(v, "v", dev, heads, d)
+    if nv != n or (not isinstance(slots, int) and slots.numel() < n):
+        raise ValueError(f"{n} keys, {nv} values and {slots if isinstance(slots, int) else slots.numel()} slots")
+    rows = geom.pages * heads * geom.page_tokens
+    code = lib.vattn_cache_append(geom, kp, ks, vp, vs, _on(slots, dev, "slots", _I32, n * 4), n,
+                                  _on(kcache, dev, "kcache", _BYTES, rows * d), _on(vcache, dev, "vcache", _BYTES, rows * d),
+                                  _on(kscale, dev, "kscale", _F32, rows // 4), _on(vscale, dev, "vscale", _F32, rows // 4),
+                                  _current_stream(stream, dev))
+    if code:
+        _check(code)
 
 
 def vattn_cache_workspace_size(geom: CacheGeom, n_tokens: int, max_new: int) -> int:
@@ -443,13 +483,25 @@ def vattn_cache_fwd(geom: CacheGeom, q, q_starts, kv_lens, block_table, kcache, 
                     max_new: int, o, lse=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
     """Attention of q [tokens, q_heads, d] (bf16, may be a slice of a fused projection) over the cache."""
     dev = _device(q)
-    if workspace is not None and not ws_bytes:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    qp, stride, n = _tokens(q, "q", dev)
-    _check(lib.vattn_cache_fwd(ctypes.byref(geom), qp, stride, _on(q_starts, dev), _on(kv_lens, dev),
-                               _on(block_table, dev), _on(kcache, dev), _on(vcache, dev), _on(kscale, dev),
-                               _on(vscale, dev), scale, n, max_new, _on(o, dev), _on(lse, dev), _on(workspace, dev),
-                               ws_bytes, _current_stream(stream, dev)))
+    if workspace is not None and not isinstance(workspace, int):
+        size = workspace.numel() * workspace.element_size()
+        if ws_bytes > size:
+            raise ValueError(f"workspace: {size} bytes, but ws_bytes is {ws_bytes}")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the call's device")
+        workspace, ws_bytes = workspace.data_ptr(), ws_bytes or size
+    heads, d, lens = geom.q_heads, geom.head_dim, geom.streams * 4
+    qp, stride, n = _tokens(q, "q", dev, heads, d)
+    rows = geom.pages * geom.kv_heads * geom.page_tokens
+    code = lib.vattn_cache_fwd(geom, qp, stride, _on(q_starts, dev, "q_starts", _I32, lens + 4),
+                               _on(kv_lens, dev, "kv_lens", _I32, lens),
+                               _on(block_table, dev, "block_table", _I32, lens * geom.table_width),
+                               _on(kcache, dev, "kcache", _BYTES, rows * d), _on(vcache, dev, "vcache", _BYTES, rows * d),
+                               _on(kscale, dev, "kscale", _F32, rows // 4), _on(vscale, dev, "vscale", _F32, rows // 4),
+                               scale, n, max_new, _on(o, dev, "o", _BF16, n * heads * d * 2),
+                               _on(lse, dev, "lse", _F32, n * heads * 4), workspace, ws_bytes, _current_stream(stream, dev))
+    if code:
+        _check(code)
 
 
 def vattn_get_status(stream=None) -> int:
