@@ -466,6 +466,10 @@ int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_st
  *   workspace >= vattn_cache_workspace_size(geom, n_tokens, max_new): partial
  *     results of keys that are split over several thread blocks.  Two calls
  *     that may overlap on the GPU need a workspace each.
+ * V's scales that one query sees may lie up to a factor of 2^100 apart, which
+ * holds for every v of magnitude up to 448 * 2^60 (a block of zeros has scale
+ * 2^-40).  The weights are summed relative to them, so farther apart the tokens
+ * of the smaller scales drop out of O and LSE.
  * A query row with a NaN or an infinity gives a NaN row, unless it sees nothing.
  * Deterministic. */
 int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_stride, const int32_t* q_starts,
