@@ -29,13 +29,11 @@ def plan(page_tokens, width, pages, new_tokens, kv_lens, table, free_pages, n_fr
                 [-1] * max_tokens, [status, 0, n_free, max([0, *map(int, kv_lens)])])
 
     worst = 0
-    for s, (n, old) in enumerate(zip(new_tokens, lens)):
+    for n, old in zip(new_tokens, lens):
         if old < 0 or old > width * page_tokens:
             worst = max(worst, 4)
         elif n >= 0 and old + n > width * page_tokens:
             worst = max(worst, 2)
-        elif n > 0 and old % page_tokens and not 0 <= table[s, old // page_tokens] < pages:
-            worst = 4                    # the page that the stream goes on filling
     if worst:
         return stop(worst)
     stack = [int(x) for x in free[:max(n_free, 0)]]
@@ -53,8 +51,9 @@ def plan(page_tokens, width, pages, new_tokens, kv_lens, table, free_pages, n_fr
     need = sum(-(-(old + n) // page_tokens) - -(-old // page_tokens) for n, old in zip(new_tokens, lens) if n >= 0)
     if need > len(stack):
         return stop(1)
-    if not all(0 <= x < pages for x in stack[len(stack) - need:]):
-        return stop(4)
+    filled = [table[s, old // page_tokens] for s, (n, old) in enumerate(zip(new_tokens, lens)) if n > 0 and old % page_tokens]
+    if not all(0 <= x < pages for x in stack[len(stack) - need:] + filled):
+        return stop(4)                   # a page to be handed out, or gone on filling
     starts, slots = [0], []
     for s, n in enumerate(new_tokens):
         old, n = lens[s], int(n)

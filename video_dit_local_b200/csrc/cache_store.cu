@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const 
 
   // sums and the verdict, before anything is written
   long long give = 0, take = 0, add = 0;
-  int longest = 0, worst = VATTN_PLAN_OK;
+  int longest = 0, worst = VATTN_PLAN_OK, filled = 0;
+  bool bad = false, fills = false;
   for (int s = s0; s < s1; ++s) {
     const int len = a.kv_lens[s], n = a.new_tokens[s];
     if (len < 0 || len > cap) {
@@ -85,9 +86,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const 
       take += r.take;
       add += r.add;
       longest = max(longest, n < 0 ? 0 : len + r.add);
-      // the page that the stream goes on filling
-      if (r.add > 0 && (len & (g.page_tokens - 1)) && !in_pool(a.table[(long long)s * g.width + (len >> g.page_shift)]))
-        worst = VATTN_PLAN_BAD_STATE;
+      // the page that the stream goes on filling (looked at later on: nothing waits for it here)
+      bad |= fills && !in_pool(filled);
+      fills = r.add > 0 && (len & (g.page_tokens - 1));
+      if (fills) filled = a.table[(long long)s * g.width + (len >> g.page_shift)];
     }
   }
   const long long my_give = give, my_take = take, my_add = add;
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Geom g, const 
   __syncthreads();
 
   if (verdict == VATTN_PLAN_OK) {
-    bool bad = false;
+    bad |= fills && !in_pool(filled);
     // what is taken from below the pages that ending streams give
     for (int i = (int)tot_give + t; i < (int)tot_take; i += PLAN_THREADS)
       bad |= !in_pool(a.free_pages[n_free + (int)tot_give - 1 - i]);
