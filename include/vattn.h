@@ -466,6 +466,11 @@ int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_st
  *   workspace >= vattn_cache_workspace_size(geom, n_tokens, max_new): partial
  *     results of keys that are split over several thread blocks.  Two calls
  *     that may overlap on the GPU need a workspace each.
+ * Queries: with at most 16 rows of a stream and kv head (max_new * q_heads /
+ * kv_heads) an element keeps its 8 significant bits down to 2^-29 of its row's
+ * largest; with more rows it is exact to 2^-17 of the largest, so elements far
+ * below that one keep fewer bits.  Weights are rounded to 11 bits before they
+ * meet V, sums are float32.
  * V's scales that one query sees may lie up to a factor of 2^100 apart, which
  * holds for every v of magnitude up to 448 * 2^60 (a block of zeros has scale
  * 2^-40).  The weights are summed relative to them, so farther apart the tokens

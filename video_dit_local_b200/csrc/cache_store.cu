@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(256) slots_kernel(const Geom g, const CachePla
 // rows are read once into registers (all loads in flight together), the block's
 // absmax gives the scale exponent, and the bytes leave in whole cache rows.
 // Bound by HBM: 4 d bytes in, 2 d bytes out per token and kv head (two 1080p
-// frames, 24 heads of 128, from a fused projection: 51 us, 6.2 TB/s).  That
+// frames, 24 heads of 128, from a fused projection: 52-55 us, 6 TB/s).  That
 // leaves about 600 instructions a block: a block of sixteen finite new tokens,
 // which is what a frame is made of, takes a path without predicates.
 // ---------------------------------------------------------------------------
@@ -445,10 +445,12 @@ cudaError_t launch_cache_plan(const cache::Geom& g, const CachePlanArgs& a, cuda
 cudaError_t launch_cache_append(const cache::Geom& g, const CacheAppendArgs& a, cudaStream_t st) {
   using namespace cache;
   // Tokens a warp looks through for blocks to take.  16: one warp a block of a
-  // long run of tokens, where 1 would start 15 idle warps for each that works
-  // (two 1080p frames, 24 heads of 128: 85 us against 182, with eight warps a block); 1: blocks of single
-  // tokens side by side instead of one after the other, as long as 16 would
-  // leave the GPU short of warps.
+  // long run of tokens, where 1 starts 15 idle warps for each that works (24
+  // heads of 128, 10,000 token-blocks: 23 us against 72 for one run of tokens,
+  // 22 against 54 for chunks of 1 to 90); 1: blocks of short chunks side by side
+  // instead of one after the other, as long as 16 leaves the GPU short of warps
+  // (500 blocks: 5.0 us against 5.9 for such chunks).  At 1000 blocks the two
+  // meet for such chunks; runs are faster with 16 at any size.
   const int span = (long long)a.n_tokens / 16 * g.kv_heads >= 148 * 16 ? 16 : 1;
   const long long warps = (long long)((a.n_tokens + span - 1) / span) * g.kv_heads;
   const long long blocks = (warps + APPEND_WARPS - 1) / APPEND_WARPS;
