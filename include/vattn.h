@@ -458,7 +458,7 @@ int vattn_cache_append(const vattn_cache_geom* geom, const void* k, int64_t k_st
 
 /* Attention of the streams' new tokens over the cache (append them first):
  * S = scale * q.k over the tokens that the mask leaves, LSE = ln sum exp(S),
- * O = sum exp(S - LSE) v.  scale must be positive and finite.
+ * O = sum exp(S - LSE) v.  scale must be positive, scale * log2(e) finite.
  *   max_new: no stream has more new tokens than this (the caller knows it
  *     without reading device memory); it selects the kernel and sizes the grid;
  *   o bf16 [n_tokens][q_heads][d], lse float32 [n_tokens][q_heads] or NULL.

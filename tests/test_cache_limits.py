@@ -55,6 +55,15 @@ def test_counts_past_the_limits_are_refused_before_a_launch():
     assert V.vattn_cache_workspace_size(geom(2, 2), TOP, TOP) > 0
 
 
+def test_a_scale_whose_base_2_form_is_infinite_is_refused():
+    import video_dit_local_b200 as V
+    g = V.make_cache_geom(1, 1, 1, 64, 4, 16, 4)
+    for scale in (2.4e38, 3.4e38):          # finite; times log2(e) past the largest float
+        with pytest.raises(V.VattnError) as e:
+            V.vattn_cache_fwd(g, Rows(5, 1), 16, 16, 16, 16, 16, 16, 16, scale, 3, 16, 16, 16, 1 << 40, stream=0)
+        assert e.value.code == V.binding.VATTN_ERR_INVALID_ARG
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("max_tokens", [TOP, TOP - 254, TOP - 255, TOP - 256])
 def test_plan_lists_as_many_slots_as_there_can_be(max_tokens):

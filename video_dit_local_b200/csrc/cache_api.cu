@@ -215,7 +215,9 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   if (r) return r;
   if ((r = check_tokens(n_tokens))) return r;
   if (max_new < 0) return fail(VATTN_ERR_INVALID_ARG, "max_new must be >= 0");
-  if (!(scale > 0.f) || std::isinf(scale)) return fail(VATTN_ERR_INVALID_ARG, "scale must be positive and finite");
+  const float scale_log2 = scale * 1.4426950408889634f;  // the kernels' exponentials are of base 2
+  if (!(scale > 0.f) || std::isinf(scale_log2))
+    return fail(VATTN_ERR_INVALID_ARG, "scale must be positive, and scale * log2(e) finite");
   if (max_new > n_tokens) max_new = n_tokens;
   if ((r = check_rows(g, max_new))) return r;
   if (g.streams == 0 || n_tokens == 0 || max_new == 0) return ok();
@@ -248,7 +250,7 @@ int vattn_cache_fwd(const vattn_cache_geom* geom, const void* q, int64_t q_strid
   p.vc = (const uint8_t*)vcache;
   p.ks = kscale;
   p.vs = vscale;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.n_tokens = (int)n_tokens;
   p.max_new = (int)max_new;
   p.o = (__nv_bfloat16*)o;
